@@ -97,7 +97,8 @@ typedef enum {
     QMM_ERR_TIMEOUT = -6,     /* a device-side pipeline wait gave up (status word) */
     QMM_ERR_UNSUPPORTED = -7, /* a valid request this version does not implement */
     QMM_ERR_NOMEM = -8,       /* a workspace allocation failed */
-    QMM_ERR_EXPERT = -9       /* an expert id outside [0, n_experts) (status word) */
+    QMM_ERR_EXPERT = -9,      /* an expert id outside [0, n_experts) (status word) */
+    QMM_ERR_PAGE = -10        /* a slot, page id or length outside the cache (status word) */
 } qmm_status;
 
 typedef struct qmm_matrix *qmm_t;
@@ -321,6 +322,153 @@ QMM_API qmm_status qmm_gemv_q8k_group(const qmm_t *hs, int32_t n, const void *xq
 QMM_API qmm_status qmm_gemv_q8k_fused(qmm_t h, const float *x, float *y, qmm_stream stream);
 QMM_API qmm_status qmm_gemv_q8k_fused_group(const qmm_t *hs, int32_t n, const float *x,
                                             float *const *ys, qmm_stream stream);
+
+/* ---- The decode step around the products ------------------------------
+ * What a decode step does between the quantized products: new keys and
+ * values into a paged cache ("Frink Inference: the Rust alternative to
+ * llama.cpp", "The goal, stated once": continuous batching over paged KV),
+ * the attention of each sequence's new token over it, and the adjustment of
+ * the last product's logits before sampling.  Plain types carry their GGUF
+ * ids. */
+typedef enum { QMM_F32 = 0, QMM_F16 = 1, QMM_BF16 = 30 } qmm_dtype;
+
+typedef struct qmm_kv_cache *qmm_kv_t;
+
+/* Describe a paged cache of n_pages pages of page_size slots (any size >= 1)
+ * for n_kv_heads heads of head_dim values (64, 96, 128, 192 or 256; others:
+ * QMM_ERR_UNSUPPORTED), in two borrowed buffers of qmm_kv_bytes() bytes each,
+ * 16-byte aligned, of one layout:
+ *   type QMM_F16, QMM_BF16:  [page][head][slot][head_dim]
+ *   type QMM_Q8_0:  int8 codes [page][head][slot][head_dim], then fp16 scales
+ *     [page][head][slot][S], S = head_dim/32 rounded up to even (the odd one
+ *     is padding and never read); value d = code[d] * scale[d/32].  Q8_0's
+ *     blocks with the scales in a plane of their own.
+ * Slot numbers are page * page_size + offset.  n_pages * page_size *
+ * n_kv_heads <= 2^32 - 1.  Allocates the handle's workspace (the attention's
+ * partial results, about 5 MB at head_dim 128) and status word; synchronises.
+ * Calls on one handle must be ordered on one stream, as for qmm_t.  No later
+ * call allocates: they can be captured into a CUDA graph. */
+QMM_API qmm_status qmm_kv_create(int32_t type, int64_t n_pages, int32_t page_size,
+                                 int32_t n_kv_heads, int32_t head_dim, void *k_dev, void *v_dev,
+                                 qmm_kv_t *out);
+
+/* Bytes of each of the two buffers of such a cache, or a negative qmm_status. */
+QMM_API int64_t qmm_kv_bytes(int32_t type, int64_t n_pages, int32_t page_size,
+                             int32_t n_kv_heads, int32_t head_dim);
+
+/* Free the handle and its workspace (synchronises the device first). */
+QMM_API qmm_status qmm_kv_destroy(qmm_kv_t kv);
+
+/* Rotary positions with 1 to 4 axes (text; or time, height and width of
+ * images and video).  Pair i < n_rot/2 of a head is dims (i, i + n_rot/2)
+ * (QMM_ROPE_HALVES) or (2i, 2i+1) (QMM_ROPE_ADJACENT); dims from n_rot on
+ * pass through.  The first sections[0] pairs turn by axis 0, the next
+ * sections[1] by axis 1, ...; the n_axes sections sum to n_rot/2.  Pair i of
+ * token t turns by the angle fl32((float)pos[axis][t] * inv_freq[i]): the
+ * product rounded to fp32 is the definition, as models are trained with.
+ * inv_freq: n_rot/2 fp32 on the device (so every scaling of frequencies is a
+ * matter of filling it). */
+#define QMM_ROPE_HALVES 0
+#define QMM_ROPE_ADJACENT 1
+typedef struct {
+    int32_t n_rot;       /* rotated dims, even, 0 (none) to head_dim */
+    int32_t pairing;     /* QMM_ROPE_HALVES or QMM_ROPE_ADJACENT */
+    int32_t n_axes;      /* 1 to 4 */
+    int32_t sections[4]; /* pairs of each axis */
+    const float *inv_freq;
+} qmm_rope;
+
+/* Rotate and store T new tokens in one launch.  k, v: [T, n_kv_heads,
+ * head_dim], rows of tokens ldk, ldv elements apart; q (may be NULL: nothing
+ * is done for it): [T, n_q_heads, head_dim], ldq apart, rotated into q_out
+ * (ldqo apart; may be q itself with ldqo == ldq, and must not overlap it
+ * otherwise).  All of one type, QMM_F32, QMM_F16 or QMM_BF16, every row on a
+ * 16-byte boundary.  Token t's k (rotated) and v go to slot slots[t], rounded
+ * once to the cache's type (nearest even; Q8_0: scale = max|x|/127 of each 32
+ * values in fp32, code = round-half-even(x * (1/scale)), the scale kept in
+ * fp16); slots[t] < 0 stores nothing (its q is still rotated), a slot past
+ * the cache stores nothing and sets QMM_ERR_PAGE in the status word.  Slots
+ * of one call are distinct.  pos: [n_axes, T] int32.  rope NULL or n_rot 0:
+ * nothing is rotated, pos may be NULL.  The rotation is computed in fp32,
+ * each product and sum rounded once. */
+QMM_API qmm_status qmm_kv_append(qmm_kv_t kv, int32_t dtype, int64_t T, const void *k, int64_t ldk,
+                                 const void *v, int64_t ldv, const int64_t *slots, const void *q,
+                                 int64_t ldq, int32_t n_q_heads, void *q_out, int64_t ldqo,
+                                 const int32_t *pos, const qmm_rope *rope, qmm_stream stream);
+
+/* Values of T slots out of the cache: k_out, v_out (either may be NULL)
+ * [T, n_kv_heads, head_dim] in dtype, rows ldk, ldv elements apart on 16-byte
+ * boundaries.  A negative slot gives zeros; one past the cache gives zeros
+ * and sets QMM_ERR_PAGE. */
+QMM_API qmm_status qmm_kv_read(qmm_kv_t kv, int32_t dtype, int64_t T, const int64_t *slots,
+                               void *k_out, int64_t ldk, void *v_out, int64_t ldv,
+                               qmm_stream stream);
+
+typedef struct {
+    float scale;        /* multiplies q.k; finite */
+    float softcap;      /* 0: none; else s = softcap * tanh(s / softcap) */
+    int32_t window;     /* 0: every key; else the newest `window` keys */
+    const float *alibi; /* NULL, or n_q_heads slopes on the device: after the
+                           cap, s_j += slope * (j - (len - 1)) */
+} qmm_attn;
+
+/* Attention of one new token of each of n_seqs sequences over its cached
+ * keys: out = sum_j softmax(s)_j v_j over the keys j in [max(0, len -
+ * window), len), s_j = scale * q.k_j with the options above.  q, out:
+ * [n_seqs, n_q_heads, head_dim] of one type, rows ldq, ldo elements apart on
+ * 16-byte boundaries; head h reads kv head h / (n_q_heads / n_kv_heads).
+ * Key j of sequence b is slot page_table[b * ld_table + j / page_size] *
+ * page_size + j % page_size; only the pages of keys in range are looked at.
+ * lens[b] counts the new token's own key where it was appended before.  A
+ * sequence without keys (len 0) gives zeros.  lse (may be NULL): [n_seqs,
+ * n_q_heads] fp32, ln sum_j exp(s_j), -inf without keys (what joining with
+ * attention over other keys needs).  Lengths are read on the device: a
+ * captured call serves growing sequences.  A page id outside [0, n_pages)
+ * leaves its keys out, a length that is negative or beyond ld_table pages is
+ * cut to fit; either sets QMM_ERR_PAGE in the status word.  Slots out of
+ * range are never read, whatever they hold.
+ * Computed in fp32 precision throughout (the cache's values are exact
+ * operands); bitwise repeatable for the same lengths. */
+QMM_API qmm_status qmm_attn_decode(qmm_kv_t kv, int32_t dtype, int64_t n_seqs, int32_t n_q_heads,
+                                   const void *q, int64_t ldq, const int32_t *page_table,
+                                   int64_t ld_table, const int32_t *lens, const qmm_attn *attn,
+                                   void *out, int64_t ldo, float *lse, qmm_stream stream);
+
+/* Read and clear the cache handle's status word (synchronises the device). */
+QMM_API qmm_status qmm_kv_get_status(qmm_kv_t kv);
+
+/* What is done to each row of logits; every pointer is a device pointer and
+ * may be NULL (that part is left out). */
+typedef struct {
+    /* Penalties: c = how often v occurs in the row's history (row b's tokens
+     * are history[history_offsets[b] .. history_offsets[b+1]); n_rows + 1
+     * offsets; ids outside the vocabulary, such as -1 padding, are ignored).
+     * Where c > 0: z = z > 0 ? z / repeat[b] : z * repeat[b], then
+     * z -= presence[b] + frequency[b] * c.  NULL: 1, 0, 0. */
+    const int32_t *history;
+    const int64_t *history_offsets;
+    int64_t n_history; /* entries of `history`: offsets are clamped to it */
+    const float *repeat, *presence, *frequency;
+    /* Then biases: z += the values of the row's entries whose id is v, added
+     * up in list order (ragged like the history). */
+    const int32_t *bias_ids;
+    const float *bias_values;
+    const int64_t *bias_offsets;
+    int64_t n_biases;
+    /* Then the mask: bit v % 32 of word v / 32 of row b clear: z = -inf.
+     * Rows ld_mask words apart; ld_mask 0: one row for all. */
+    const uint32_t *mask;
+    int64_t ld_mask;
+} qmm_logit_rules;
+
+/* out[b, v] = logits[b, v] under the rules, one pass, any n_vocab up to 2^26;
+ * fp32 arithmetic in the order given, rounded once to the type (QMM_F32,
+ * QMM_F16, QMM_BF16).  Rows ld, ldo elements apart, aligned to elements.  out
+ * may be logits itself (ldo == ld); it must not overlap it otherwise.  A row
+ * whose mask allows nothing is -inf throughout. */
+QMM_API qmm_status qmm_logits_adjust(int32_t dtype, int64_t n_rows, int64_t n_vocab,
+                                     const void *logits, int64_t ld, const qmm_logit_rules *rules,
+                                     void *out, int64_t ldo, qmm_stream stream);
 
 /* Read and clear the handle's device status word (synchronises the handle's
  * last stream first).  QMM_OK when no device-side fault was recorded. */

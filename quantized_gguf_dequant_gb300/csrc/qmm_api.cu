@@ -627,6 +627,19 @@ qmm_status noalloc_fail(qmm_status code, const char *fmt, ...)
     return code;
 }
 
+void clear_error() { g_err.clear(); }
+
+qmm_status record_error(qmm_status code, const char *fmt, ...)
+{
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof(buf), fmt, ap);
+    va_end(ap);
+    g_err = buf;
+    return code;
+}
+
 qmm_status noalloc_check(int fmt, int64_t N, int64_t K, const void *w, const float *x,
                          const float *y)
 {
@@ -658,7 +671,7 @@ extern "C" {
 
 const char *qmm_last_error(void) { return g_err.c_str(); }
 
-int32_t qmm_version(void) { return 100; }
+int32_t qmm_version(void) { return 200; }
 
 int64_t qmm_launch_count(void) { return qmm::g_launches.load(std::memory_order_relaxed); }
 

@@ -16,6 +16,9 @@ constexpr int kMaxGroup = 8;
 // Device status-word bits (see qmm_get_status).
 constexpr unsigned kStatusTimeoutBit = 1u;
 constexpr unsigned kStatusBadExpertBit = 2u;
+constexpr unsigned kStatusBadSlotBit = 4u;    // a cache slot outside the cache
+constexpr unsigned kStatusBadPageBit = 8u;    // a page id outside the cache
+constexpr unsigned kStatusBadLengthBit = 16u; // a length beyond its row of the page table
 
 struct Matrix {
     int fmt = 0;
@@ -387,6 +390,108 @@ struct Q8kArgs {
 size_t q8k_smem(int64_t K);
 cudaError_t launch_quantize_q8k(const float *x, int64_t K, uint8_t *out, cudaStream_t s);
 cudaError_t launch_gemv_q8k(const Q8kArgs &a, int sm_count, cudaStream_t s);
+
+// --------------------------------------------------------------- paged key-value cache
+// Division by an invariant (kv_cache.cuh fast_div).
+struct FastDiv {
+    uint32_t d, mul, shift;
+};
+FastDiv make_fast_div(uint32_t d);
+
+struct KvView {
+    uint8_t *k, *v;       // rows of values (f16, bf16) or codes (Q8_0)
+    void *ks, *vs;        // Q8_0: the scales (fp16), kv_scales_per_row() a row
+    FastDiv page;         // divides by the page size
+    uint32_t n_pages, n_rows;  // n_rows = pages * heads * page size (< 2^32)
+    int page_size, n_heads, D;
+};
+
+struct KvCache {
+    int type = 0;         // QMM_F16, QMM_BF16 or QMM_Q8_0
+    KvView view;
+    int device = 0, sm_count = 0;
+    float *ws = nullptr;  // attention partials: two per block
+    size_t ws_bytes = 0;
+    unsigned *tickets = nullptr;  // one per block
+    unsigned *status = nullptr;
+    int max_blocks = 0;
+};
+
+struct AppendArgs {
+    KvView c;
+    int type, dtype;
+    int64_t T;
+    const void *q, *k, *v;
+    void *q_out;
+    int64_t ldq, ldqo, ldk, ldv;  // elements between tokens
+    int n_q;                      // query heads (0: no q)
+    const int64_t *slots;
+    const int32_t *pos;           // [n_axes][T]
+    const float *inv_freq;
+    int n_rot, adjacent, n_axes;
+    int axis_end[4];              // cumulative pairs
+    unsigned *status;
+};
+cudaError_t launch_kv_append(const AppendArgs &a, int sm_count, cudaStream_t s);
+
+struct KvReadArgs {
+    KvView c;
+    int type, dtype;
+    int64_t T;
+    const int64_t *slots;
+    void *k, *v;                  // either may be null
+    int64_t ldk, ldv;
+    unsigned *status;
+};
+cudaError_t launch_kv_read(const KvReadArgs &a, int sm_count, cudaStream_t s);
+
+// Attention of one new token per sequence (attn_decode.cu).
+constexpr int kAttnHeads = 8;      // query heads of one kv head that a block takes together
+struct AttnArgs {
+    KvView c;
+    int type, dtype;
+    int n_seqs, n_q;
+    const void *q;
+    void *out;
+    int64_t ldq, ldo;
+    const int32_t *table;
+    int64_t ld_table;
+    const int32_t *lens;
+    float scale, softcap;
+    int window;
+    const float *alibi;
+    float *lse;
+    float *ws;
+    unsigned *tickets, *status;
+    int max_blocks;
+};
+bool attn_takes_head_dim(int D);
+size_t attn_partial_floats(int D);  // floats of one partial result
+cudaError_t launch_attn_decode(const AttnArgs &a, int sm_count, cudaStream_t s);
+
+// --------------------------------------------------------------- logits
+struct LogitsArgs {
+    int dtype;
+    int64_t B, V;
+    const void *in;
+    void *out;
+    int64_t ld_in, ld_out;
+    const int32_t *history;
+    const int64_t *history_offsets;
+    int64_t n_history;
+    const float *repeat, *presence, *frequency;
+    const int32_t *bias_ids;
+    const float *bias_values;
+    const int64_t *bias_offsets;
+    int64_t n_biases;
+    const uint32_t *mask;
+    int64_t ld_mask;
+};
+cudaError_t launch_logits_adjust(const LogitsArgs &a, int sm_count, cudaStream_t s);
+
+// Recording a refusal sentence for qmm_last_error() from other files.
+void clear_error();
+qmm_status record_error(qmm_status code, const char *fmt, ...);
 
 // --------------------------------------------------------------- no-allocation entry
 // Layout of qmm_gemv_noalloc's static scratch: [status word, padded to 256 B]
