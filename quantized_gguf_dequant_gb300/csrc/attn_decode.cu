@@ -58,6 +58,14 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 16;  // keys per tile (the instruction's k and two n)
 constexpr int kH = kAttnHeads;
+constexpr int kLens = 512;  // lengths kept in shared memory
+// The fixed part of an item's time in a block (its first loads, its joins), in
+// the time of 16-key tiles; blocks get equal shares of tiles and these.
+constexpr int kItemCost = 12;
+// A block takes at least so much: splitting an item costs a join, which is
+// worth it from about twenty saved tiles on.
+constexpr int kMinUnits = 36;
+constexpr int kStatic = 2560;  // the kernel's static shared memory, at most
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 enum Kind { kF16, kBF16, kQ8 };
@@ -67,16 +75,18 @@ struct AttnParams {
     int group;          // query heads per kv head
     int head_tiles;     // ceil(group / 8)
     int items;          // kv heads * head tiles
-    int min_tiles;      // tiles a block takes at least
+    int min_units;      // units (16-key tiles, and kItemCost an item) a block takes at least
 };
 
 template <Kind KIND, int D>
 struct Shape {
     static constexpr int ROWB = KIND == kQ8 ? D : 2 * D;           // bytes of a row
-    // Row strides in shared memory: 16 bytes of padding put the eight rows of
-    // an ldmatrix in different banks; Q8_0 rows of 32 or 96 mod 128 bytes
-    // spread its 8-byte loads.
-    static constexpr int RS = KIND == kQ8 ? ROWB + (D % 64 == 0 ? 32 : 0) : ROWB + 16;
+    // Rows in shared memory: 16-byte chunk c of row r sits at c ^ (r & 7) where
+    // rows are whole 128 bytes, else rows are padded by 16 bytes; either way the
+    // eight rows of an ldmatrix lie in different banks.  Q8_0 rows of 32 or 96
+    // mod 128 bytes spread its 8-byte loads.
+    static constexpr bool SWZ = KIND != kQ8 && D % 64 == 0;
+    static constexpr int RS = KIND == kQ8 ? ROWB + (D % 64 == 0 ? 32 : 0) : ROWB + (SWZ ? 0 : 16);
     static constexpr int SP = kv_scales_per_row(D);
     static constexpr int SCB = KIND == kQ8 ? SP * 2 : 0;           // bytes of a row's scales
     static constexpr int STAGE = 2 * kTile * (RS + SCB);
@@ -85,14 +95,22 @@ struct Shape {
     static constexpr int QFRAG = KSTEPS * 512 + (KIND == kBF16 ? KSTEPS * 256 : 0);
     static constexpr int OSTRIDE = D + 4;
     static constexpr int JOIN = kWarps * kH * (OSTRIDE + 2) * 4;
-    // Two blocks on an SM where two stages a warp still fit in half of it.
-    static constexpr int HALF = 113 * 1024 - QFRAG - 1024, WHOLE = 226 * 1024 - QFRAG - 1024;
-    static constexpr bool TWO = 2 * kWarps * STAGE <= HALF;
-    static constexpr int FIT = (TWO ? HALF : WHOLE) / (kWarps * STAGE);
+    // Resident blocks an SM: as many as leave two stages a warp (and, for the
+    // registers, four): a warp's work on a tile is a chain of dependent
+    // steps that other warps have to cover.
+    static constexpr int LEAST = QFRAG + 2 * kWarps * STAGE + kStatic + 1024;
+    static constexpr int BLOCKS = 228 * 1024 / LEAST < 4 ? 228 * 1024 / LEAST : 4;
+    static constexpr int FIT =
+        (228 * 1024 / BLOCKS - QFRAG - kStatic - 1024) / (kWarps * STAGE);
     static constexpr int STAGES = FIT < 6 ? FIT : 6;
     static constexpr int RING = kWarps * STAGES * STAGE;
     static constexpr int SMEM = QFRAG + (RING > JOIN ? RING : JOIN);
     static_assert(STAGES >= 2, "ring");
+    // Address of 16-value column ks of a row, from that of column 0.
+    static __device__ __forceinline__ uint32_t chunk_at(uint32_t row, int ks)
+    {
+        return SWZ ? (row ^ ((ks & 3) * 32)) + (ks >> 2) * 128 : row + ks * 32;
+    }
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -210,14 +228,21 @@ __device__ __forceinline__ float load_any(const void *p, int64_t i, int dtype)
            : dtype == QMM_F16 ? load_io<__half>(p, i)
                               : load_io<__nv_bfloat16>(p, i);
 }
-__device__ __forceinline__ void store_any(void *p, int64_t i, float v, int dtype)
+__device__ __forceinline__ void store4_any(void *p, int64_t i, float4 v, int dtype)
 {
     if (dtype == QMM_F32)
-        store1(static_cast<float *>(p) + i, v);
+        store4(static_cast<float *>(p) + i, v);
     else if (dtype == QMM_F16)
-        store1(static_cast<__half *>(p) + i, v);
+        store4(static_cast<__half *>(p) + i, v);
     else
-        store1(static_cast<__nv_bfloat16 *>(p) + i, v);
+        store4(static_cast<__nv_bfloat16 *>(p) + i, v);
+}
+__device__ __forceinline__ void add4(float4 &s, float f, float4 v)
+{
+    s.x += f * v.x;
+    s.y += f * v.y;
+    s.z += f * v.z;
+    s.w += f * v.w;
 }
 
 // The dim of a head that lane group g's accumulator pair x of value tile ds holds.
@@ -240,15 +265,16 @@ __device__ __forceinline__ float value_at(const uint8_t *data, const void *scale
 }
 
 template <Kind KIND, int D>
-__global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ AttnParams P)
+__global__ void __launch_bounds__(kThreads, Shape<KIND, D>::BLOCKS) attn_kernel(const __grid_constant__ AttnParams P)
 {
     using S = Shape<KIND, D>;
     using H = Half<KIND>;
     constexpr int STAGES = S::STAGES;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t scan[kThreads];
-    __shared__ int64_t found[2];   // {start of the sequence's tiles, tiles in all}
+    __shared__ int64_t warp_units[kWarps];
+    __shared__ int64_t found_at;   // first tile of the sequence that the block starts in
     __shared__ int found_seq;
+    __shared__ int lens[kLens];
     __shared__ unsigned valid_ring[kWarps][STAGES];
     __shared__ int qexp[kH];
     __shared__ bool qfinite[kH];
@@ -262,50 +288,61 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
     pdl_launch_dependents();
 
     // ---- the plan: prefix sums of the sequences' tiles
-    const int per = (A.n_seqs + kThreads - 1) / kThreads;
-    const int sb0 = min(A.n_seqs, tid * per), sb1 = min(A.n_seqs, sb0 + per);
+    for (int b = tid; b < min(A.n_seqs, kLens); b += kThreads)
+        lens[b] = __ldg(A.lens + b);
+    __syncthreads();
+    auto units_of = [&](int n) { return n ? int64_t(n + kItemCost) * P.items : int64_t(0); };
+    auto len_of = [&](int b) { return b < kLens ? lens[b] : __ldg(A.lens + b); };
+    const int per_thread = (A.n_seqs + kThreads - 1) / kThreads;
+    const int sb0 = min(A.n_seqs, tid * per_thread), sb1 = min(A.n_seqs, sb0 + per_thread);
     int64_t mine = 0;
     for (int b = sb0; b < sb1; ++b) {
-        const int len = __ldg(A.lens + b);
+        const int len = len_of(b);
         const Span sp = span_of(A, len);
-        mine += int64_t(sp.n) * P.items;
+        mine += units_of(sp.n);
         if (blockIdx.x == 0 && (len < 0 || len > sp.hi))
             atomicOr(A.status, kStatusBadLengthBit);
     }
     // sequences without keys are no one's item: their outputs are zero
     for (int b = blockIdx.x; b < A.n_seqs; b += gridDim.x) {
-        if (span_of(A, __ldg(A.lens + b)).n > 0)
+        if (span_of(A, len_of(b)).n > 0)
             continue;
-        for (int i = tid; i < A.n_q * D; i += kThreads)
-            store_any(A.out, b * A.ldo + i, 0.f, A.dtype);
+        for (int i = tid; i < A.n_q * D / 4; i += kThreads)
+            store4_any(A.out, b * A.ldo + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f), A.dtype);
         if (A.lse)
             for (int i = tid; i < A.n_q; i += kThreads)
                 A.lse[int64_t(b) * A.n_q + i] = -INFINITY;
     }
-    scan[tid] = mine;
-    __syncthreads();
-    for (int o = 1; o < kThreads; o <<= 1) {
-        const int64_t v = tid >= o ? scan[tid - o] : 0;
-        __syncthreads();
-        scan[tid] += v;
-        __syncthreads();
+    int64_t upto = mine;  // units of the sequences up to this thread's
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+        upto += lane >= o ? v : 0;
     }
-    const int64_t total = scan[kThreads - 1];
+    if (lane == 31)
+        warp_units[warp] = upto;
+    __syncthreads();
+    int64_t total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        upto += w < warp ? warp_units[w] : 0;
+        total += warp_units[w];
+    }
     if (total == 0)
         return;
-    const int64_t nb =
-        max(int64_t(1), min(int64_t(gridDim.x), (total + P.min_tiles - 1) / P.min_tiles));
-    const int64_t blk = blockIdx.x;
-    if (blk >= nb)
+    // block c takes units [c * per, (c + 1) * per): unit x is block x / per's
+    const int64_t per = max(int64_t(P.min_units),
+                            int64_t((uint64_t(total) + gridDim.x - 1) / gridDim.x));
+    const int64_t blk = blockIdx.x, r0 = per * blk, r1 = min(total, r0 + per);
+    if (r0 >= total)
         return;
-    const int64_t r0 = total * blk / nb, r1 = total * (blk + 1) / nb;
-    if (r0 < scan[tid] && r0 >= scan[tid] - mine) {
-        int64_t at = scan[tid] - mine;
+    if (r0 < upto && r0 >= upto - mine) {
+        int64_t at = upto - mine;
         for (int b = sb0; b < sb1; ++b) {
-            const int64_t n = int64_t(span_of(A, __ldg(A.lens + b)).n) * P.items;
+            const int64_t n = units_of(span_of(A, len_of(b)).n);
             if (r0 < at + n) {
                 found_seq = b;
-                found[0] = at;
+                found_at = at;
                 break;
             }
             at += n;
@@ -313,24 +350,32 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
     }
     __syncthreads();
     int seq = found_seq;
-    int64_t seq_at = found[0];
-    Span sp = span_of(A, __ldg(A.lens + seq));
+    int64_t seq_at = found_at;
+    Span sp = span_of(A, len_of(seq));
 
     const uint32_t smem_base = smem_u32(smem);
+    // this lane's row and half-chunk of an ldmatrix over 16 keys x 16 values
+    const uint32_t frag_row =
+        ((lane >> 4) * 8 + (lane & 7)) * S::RS +
+        (S::SWZ ? ((lane >> 3) & 1) ^ (lane & 7) : (lane >> 3) & 1) * 16;
     const uint32_t ring = smem_base + S::QFRAG + warp * STAGES * S::STAGE;
     float *join = reinterpret_cast<float *>(smem + S::QFRAG);
     float *join_ml = join + kWarps * kH * S::OSTRIDE;
 
     for (int64_t at = r0; at < r1;) {
-        while (at >= seq_at + int64_t(sp.n) * P.items) {
-            seq_at += int64_t(sp.n) * P.items;
+        while (at >= seq_at + units_of(sp.n)) {
+            seq_at += units_of(sp.n);
             ++seq;
-            sp = span_of(A, __ldg(A.lens + seq));
+            sp = span_of(A, len_of(seq));
         }
         // the item and this block's tiles [ta, tb) of it
-        const int item = int((at - seq_at) / sp.n);
-        const int64_t item_at = seq_at + int64_t(item) * sp.n;
-        const int ta = int(at - item_at), tb = int(min(r1 - item_at, int64_t(sp.n)));
+        const int item = int(uint64_t(at - seq_at) / unsigned(sp.n + kItemCost));
+        const int64_t tiles_at = seq_at + int64_t(item) * (sp.n + kItemCost) + kItemCost;
+        const int ta = int(max(int64_t(0), at - tiles_at));
+        const int tb = int(max(int64_t(0), min(r1 - tiles_at, int64_t(sp.n))));
+        at = tiles_at + sp.n;
+        if (tb <= ta)
+            break;  // the range ends in the item's overhead: the next block starts the item
         const int kvh = item / P.head_tiles, h0 = (item % P.head_tiles) * kH;
         const int nh = min(kH, P.group - h0);
         const int head0 = kvh * P.group + h0;  // first query head
@@ -339,18 +384,13 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
 
         // ---- loading
         auto key_of = [&](int i) { return (sp.t0 + ta + warp + i * kWarps) * kTile + (lane & 15); };
+        // the page of this lane's key of tile i (a guarded load and no branch,
+        // so that several are under way at once)
         auto page_id = [&](int i) -> int {
-            if (i >= nw)
-                return -1;
             const int j = key_of(i);
-            if (j < sp.lo || j >= sp.hi)
-                return -1;
-            const int id = __ldg(table + fast_div(C.page, unsigned(j)));
-            if (unsigned(id) >= C.n_pages) {
-                atomicOr(A.status, kStatusBadPageBit);
-                return -1;
-            }
-            return id;
+            const bool in = i < nw && j >= sp.lo && j < sp.hi;
+            const int id = __ldg(table + (in ? fast_div(C.page, unsigned(j)) : 0u));
+            return in ? id : -1;
         };
         auto row_of = [&](int j, uint32_t &row) {  // (the slow paths')
             if (j < sp.lo || j >= sp.hi)
@@ -364,13 +404,15 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
         auto issue = [&](int i, int id) {
             if (i < nw) {
                 const int j = key_of(i);
-                const bool ok = id >= 0 && lane < 16;
+                const bool ok = unsigned(id) < C.n_pages;
+                if (!ok && j >= sp.lo && j < sp.hi)
+                    atomicOr(A.status, kStatusBadPageBit);
                 uint32_t row = 0;
-                if (id >= 0) {
+                if (ok) {
                     const uint32_t off = unsigned(j) - fast_div(C.page, unsigned(j)) * C.page.d;
                     row = (uint32_t(id) * unsigned(C.n_heads) + unsigned(kvh)) * C.page.d + off;
                 }
-                const unsigned valid = __ballot_sync(0xffffffffu, ok);
+                const unsigned valid = __ballot_sync(0xffffffffu, ok) & 0xffffu;
                 const int st = i % STAGES;
                 if (lane == 0)
                     valid_ring[warp][st] = valid;
@@ -382,8 +424,9 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
                     const uint64_t o =
                         uint64_t(__shfl_sync(0xffffffffu, row, r)) * S::ROWB + ch * 16;
                     const unsigned bytes = (valid >> r) & 1u ? 16u : 0u;
-                    cp16(kdst + r * S::RS + ch * 16, C.k + o, bytes);
-                    cp16(vdst + r * S::RS + ch * 16, C.v + o, bytes);
+                    const unsigned at = r * S::RS + (S::SWZ ? ch ^ (r & 7) : ch) * 16;
+                    cp16(kdst + at, C.k + o, bytes);
+                    cp16(vdst + at, C.v + o, bytes);
                 }
                 if constexpr (KIND == kQ8) {
                     constexpr int W = S::SCB / 4;  // words of a row's scales
@@ -405,6 +448,26 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
             }
             cp_commit();
         };
+        // q of head tid/16, issued ahead of everything that waits
+        float qv[D / 16];
+        {
+            const int h = tid >> 4;
+            const int64_t q0 =
+                int64_t(seq) * A.ldq + int64_t(head0 + min(h, nh - 1)) * D + (tid & 15);
+            if (A.dtype == QMM_F32) {
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+                    qv[i] = __ldg(static_cast<const float *>(A.q) + q0 + i * 16);
+            } else if (A.dtype == QMM_F16) {
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+                    qv[i] = load_io<__half>(A.q, q0 + i * 16);
+            } else {
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+                    qv[i] = load_io<__nv_bfloat16>(A.q, q0 + i * 16);
+            }
+        }
         int next_id;
         {
             int ids[STAGES];
@@ -420,12 +483,10 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
         // ---- q's pieces as A operands, by 16 threads a head
         {
             const int h = tid >> 4, lt = tid & 15;
-            float qv[D / 16];
             float mx = 0.f, sum = 0.f;  // sum: 0, or NaN where q is not finite
-            const int64_t q0 = int64_t(seq) * A.ldq + int64_t(head0 + h) * D;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
-                qv[i] = h < nh ? load_any(A.q, q0 + i * 16 + lt, A.dtype) : 0.f;
+                qv[i] = h < nh ? qv[i] : 0.f;
                 mx = fmaxf(mx, fabsf(qv[i]));
                 sum += qv[i] * 0.f;
             }
@@ -535,14 +596,13 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
                 }
             } else {
                 float c0[4] = {}, c1[4] = {};
-                const uint32_t kaddr = kb + ((lane >> 4) * 8 + (lane & 7)) * S::RS +
-                                       ((lane >> 3) & 1) * 16;
+                const uint32_t kaddr = kb + frag_row;
                 if constexpr (KIND == kBF16) {
                     // the smallest piece first: its sum is exact next to the others'
 #pragma unroll
                     for (int ks = 0; ks < S::KSTEPS; ++ks) {
                         uint32_t b[4];
-                        ldsm4(b, kaddr + ks * 32);
+                        ldsm4(b, S::chunk_at(kaddr, ks));
                         const uint2 a3 = *reinterpret_cast<const uint2 *>(
                             smem + S::KSTEPS * 512 + (ks * 32 + lane) * 8);
                         mma<KIND>(c0, a3.x, 0u, a3.y, 0u, b[0], b[1]);
@@ -552,7 +612,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
 #pragma unroll
                 for (int ks = 0; ks < S::KSTEPS; ++ks) {
                     uint32_t b[4];
-                    ldsm4(b, kaddr + ks * 32);
+                    ldsm4(b, S::chunk_at(kaddr, ks));
                     const uint4 a =
                         *reinterpret_cast<const uint4 *>(smem + (ks * 32 + lane) * 16);
                     mma<KIND>(c0, a.x, a.y, a.z, a.w, b[0], b[1]);
@@ -693,12 +753,11 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
                         u1 -= hf.y;
                     }
                 }
-                const uint32_t vaddr = vb + ((lane >> 4) * 8 + (lane & 7)) * S::RS +
-                                       ((lane >> 3) & 1) * 16;
+                const uint32_t vaddr = vb + frag_row;
 #pragma unroll
                 for (int ds = 0; ds < S::KSTEPS; ++ds) {
                     uint32_t a[4];
-                    ldsm4t(a, vaddr + ds * 32);
+                    ldsm4t(a, S::chunk_at(vaddr, ds));
                     float c[4] = {};
                     if constexpr (KIND == kBF16)
                         mma<KIND>(c, a[0], a[1], a[2], a[3], b[2][0], b[2][1]);
@@ -748,6 +807,14 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
         __syncthreads();  // every warp is done with its ring: it becomes the joining space
 
         // ---- the warps' results joined
+        auto finish = [&](int h, int d, float4 sum, float M, float tot) {
+            const float inv = tot == 0.f ? 0.f : 1.f / tot;
+            store4_any(A.out, int64_t(seq) * A.ldo + int64_t(head0 + h) * D + d,
+                       make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv), A.dtype);
+            if (A.lse && d == 0)
+                A.lse[int64_t(seq) * A.n_q + head0 + h] =
+                    tot == 0.f ? -INFINITY : (M + log2f(tot) - kBias) * kLn2;
+        };
         {
             float undo = 1.f;
             if constexpr (KIND == kQ8)
@@ -768,35 +835,35 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
         }
         __syncthreads();
         const bool whole = ta == 0 && tb == sp.n;
-        const int64_t c0 = whole ? blk : ((item_at + 1) * nb - 1) / total;
-        const int64_t c1 = whole ? blk : ((item_at + sp.n) * nb - 1) / total;
+        // blocks that share the item
+        const int64_t c0 = whole ? blk : uint64_t(tiles_at) / uint64_t(per);
+        const int64_t c1 = whole ? blk : uint64_t(tiles_at + sp.n - 1) / uint64_t(per);
         constexpr int PART = kH * (D + 2);  // floats of a partial: [8][D] sums, [8] m, [8] l
-        float *mine_ws = A.ws + (2 * blk + (at == r0 ? 0 : 1)) * PART;
-        for (int i = tid; i < kH * D; i += kThreads) {
-            const int h = i / D, d = i % D;
-            float M = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w)
-                M = fmaxf(M, join_ml[(w * kH + h) * 2]);
-            float sum = 0.f, tot = 0.f;
+        constexpr int QUADS = D / 4;
+        // A block may be the last of one item and the first of another: a
+        // partial that starts its item goes to the block's second place.
+        float *mine_ws = A.ws + (2 * blk + (ta > 0 ? 0 : 1)) * PART;
+        for (int i = tid; i < nh * QUADS; i += kThreads) {
+            const int h = i / QUADS, d = i % QUADS * 4;
+            float mw[kWarps], M = -INFINITY;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float mw = join_ml[(w * kH + h) * 2];
-                const float f = mw == -INFINITY ? 0.f : ex2(mw - M);
-                // a warp without keys holds zeros; a NaN maximum cannot be -inf
-                sum += f * join[(w * kH + h) * S::OSTRIDE + d];
+                mw[w] = join_ml[(w * kH + h) * 2];
+                M = fmaxf(M, mw[w]);
+            }
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+            float tot = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = mw[w] == -INFINITY ? 0.f : ex2(mw[w] - M);
+                add4(sum, f, *reinterpret_cast<const float4 *>(
+                                 join + (w * kH + h) * S::OSTRIDE + d));
                 tot += f * join_ml[(w * kH + h) * 2 + 1];
             }
             if (whole) {
-                if (h < nh) {
-                    store_any(A.out, int64_t(seq) * A.ldo + int64_t(head0 + h) * D + d,
-                              tot == 0.f ? 0.f : sum / tot, A.dtype);
-                    if (A.lse && d == 0)
-                        A.lse[int64_t(seq) * A.n_q + head0 + h] =
-                            tot == 0.f ? -INFINITY : (M + log2f(tot) - kBias) * kLn2;
-                }
+                finish(h, d, sum, M, tot);
             } else {
-                __stcg(mine_ws + i, sum);
+                __stcg(reinterpret_cast<float4 *>(mine_ws + h * D + d), sum);
                 if (d == 0) {
                     __stcg(mine_ws + kH * D + h, M);
                     __stcg(mine_ws + kH * D + kH + h, tot);
@@ -804,44 +871,107 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
             }
         }
         if (!whole) {
-            // ---- the item's last block joins the blocks' partials in block order
-            __threadfence();
-            __syncthreads();
-            if (tid == 0)
-                last_block = atomicAdd(A.tickets + c0, 1u) == unsigned(c1 - c0);
-            __syncthreads();
-            if (last_block) {
-                __threadfence();
-                const bool first_inside = total * c0 / nb != item_at;
-                for (int i = tid; i < nh * D; i += kThreads) {
-                    const int h = i / D;
-                    float M = -INFINITY;
-                    for (int64_t c = c0; c <= c1; ++c) {
-                        const float *w =
-                            A.ws + (2 * c + (c == c0 && first_inside ? 1 : 0)) * PART;
-                        M = fmaxf(M, __ldcg(w + kH * D + h));
-                    }
-                    float sum = 0.f, tot = 0.f;
-                    for (int64_t c = c0; c <= c1; ++c) {
-                        const float *w =
-                            A.ws + (2 * c + (c == c0 && first_inside ? 1 : 0)) * PART;
-                        const float mw = __ldcg(w + kH * D + h);
-                        const float f = mw == -INFINITY ? 0.f : ex2(mw - M);
-                        sum += f * __ldcg(w + i);
-                        tot += f * __ldcg(w + kH * D + kH + h);
-                    }
-                    store_any(A.out, int64_t(seq) * A.ldo + int64_t(head0) * D + i,
-                              tot == 0.f ? 0.f : sum / tot, A.dtype);
-                    if (A.lse && i % D == 0)
-                        A.lse[int64_t(seq) * A.n_q + head0 + h] =
-                            tot == 0.f ? -INFINITY : (M + log2f(tot) - kBias) * kLn2;
+            // ---- the item's last block joins the blocks' partials in block
+            // order; many blocks first join in groups, each group's last block
+            // leaving the group's result in the place of its first
+            const int n = int(c1 - c0) + 1, k = int(blk - c0);
+            const int gs = n <= 16 ? n : (n <= 256 ? 16 : 32);  // blocks of a group
+            float *const start = A.ws + 2 * c0 * PART;
+            auto place = [&](int c) { return start + int64_t(2 * c + (c == 0)) * PART; };
+            // Is this block the last of `of` to count on the ticket?  The
+            // barrier puts every thread's stores before thread 0's release.
+            auto last_of = [&](unsigned *ticket, int of) {
+                __syncthreads();
+                if (tid == 0) {
+                    unsigned before;
+                    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;"
+                                 : "=r"(before)
+                                 : "l"(ticket)
+                                 : "memory");
+                    last_block = before == unsigned(of - 1);
+                    if (last_block)
+                        *ticket = 0;
                 }
-                if (tid == 0)
-                    A.tickets[c0] = 0;
+                __syncthreads();
+                return last_block;
+            };
+            // Sum of `count` partials `step` blocks apart, from block `from`
+            // of the item on; sixteen are under way at once.
+            auto join_parts = [&](int from, int step, int count, int h, int d, float4 &sum,
+                                  float &M, float &tot) {
+                sum = make_float4(0.f, 0.f, 0.f, 0.f);
+                M = -INFINITY;
+                tot = 0.f;
+                for (int c = 0; c < count; c += 16) {
+                    float4 o[16];
+                    float pm[16], pl[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float *w = place(from + min(c + j, count - 1) * step);
+                        o[j] = __ldcg(reinterpret_cast<const float4 *>(w + h * D + d));
+                        pm[j] = c + j < count ? __ldcg(w + kH * D + h) : -INFINITY;
+                        pl[j] = __ldcg(w + kH * D + kH + h);
+                    }
+                    float mn = M;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        mn = fmaxf(mn, pm[j]);
+                    const float f = M == -INFINITY ? 0.f : ex2(M - mn);
+                    sum = make_float4(sum.x * f, sum.y * f, sum.z * f, sum.w * f);
+                    tot *= f;
+                    M = mn;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        if (c + j >= count)
+                            continue;
+                        const float fj = pm[j] == -INFINITY ? 0.f : ex2(pm[j] - mn);
+                        add4(sum, fj, o[j]);
+                        tot += fj * pl[j];
+                    }
+                }
+            };
+            const int grp = k / gs, first = grp * gs, size = min(gs, n - first);
+            bool mine_to_join = last_of(
+                A.tickets + (grp ? A.max_blocks + c0 + first : c0), size);
+            if (mine_to_join && gs < n) {
+                constexpr int PER = (kH * QUADS + kThreads - 1) / kThreads;
+                float4 sum[PER];
+                float M[PER], tot[PER];
+#pragma unroll
+                for (int u = 0; u < PER; ++u) {
+                    const int i = tid + u * kThreads;
+                    if (i < nh * QUADS)
+                        join_parts(first, 1, size, i / QUADS, i % QUADS * 4, sum[u], M[u], tot[u]);
+                }
+                __syncthreads();  // everything is read before the first place is overwritten
+                float *w = place(first);
+#pragma unroll
+                for (int u = 0; u < PER; ++u) {
+                    const int i = tid + u * kThreads, h = i / QUADS, d = i % QUADS * 4;
+                    if (i >= nh * QUADS)
+                        continue;
+                    __stcg(reinterpret_cast<float4 *>(w + h * D + d), sum[u]);
+                    if (d == 0) {
+                        __stcg(w + kH * D + h, M[u]);
+                        __stcg(w + kH * D + kH + h, tot[u]);
+                    }
+                }
+                mine_to_join = last_of(A.tickets + 2 * A.max_blocks + c0, (n + gs - 1) / gs);
+            }
+            if (mine_to_join) {
+                for (int i = tid; i < nh * QUADS; i += kThreads) {
+                    const int h = i / QUADS, d = i % QUADS * 4;
+                    float4 sum;
+                    float M, tot;
+                    if (gs < n)
+                        join_parts(0, gs, (n + gs - 1) / gs, h, d, sum, M, tot);
+                    else
+                        join_parts(0, 1, n, h, d, sum, M, tot);
+                    finish(h, d, sum, M, tot);
+                }
             }
         }
         __syncthreads();  // the joining space becomes the ring again
-        at = item_at + tb;
     }
 }
 
@@ -860,11 +990,12 @@ cudaError_t launch_dim(AttnParams &p, int sm_count, cudaStream_t s)
         return e;
     if (occ < 1)
         return cudaErrorInvalidConfiguration;
-    p.min_tiles = kWarps;
+    p.min_units = kMinUnits;
     const int64_t longest = std::min<int64_t>(p.a.ld_table * p.a.c.page_size, 0x7fffffe0);
-    const int64_t tiles = int64_t(p.a.n_seqs) * p.items * ((longest + kTile - 1) / kTile + 1);
+    const int64_t units =
+        int64_t(p.a.n_seqs) * p.items * ((longest + kTile - 1) / kTile + 1 + kItemCost);
     int64_t grid = std::min<int64_t>(int64_t(occ) * sm_count, p.a.max_blocks);
-    grid = std::max<int64_t>(1, std::min<int64_t>(grid, tiles / p.min_tiles + 1));
+    grid = std::max<int64_t>(1, std::min<int64_t>(grid, units / p.min_units + 1));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(grid));
     cfg.blockDim = dim3(kThreads);

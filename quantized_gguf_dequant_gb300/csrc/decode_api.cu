@@ -191,7 +191,7 @@ qmm_status qmm_kv_create(int32_t type, int64_t n_pages, int32_t page_size, int32
             return cuda_error(e, fn);
         }
         c->max_blocks = c->sm_count * kBlocksPerSm;
-        const size_t words = size_t(c->max_blocks) + 64;  // tickets, status word
+        const size_t words = size_t(c->max_blocks) * 3 + 64;  // tickets, status word
         c->ws_bytes = size_t(2) * c->max_blocks * qmm::attn_partial_floats(head_dim) * 4;
         void *p = nullptr;
         e = cudaMalloc(&p, c->ws_bytes + words * 4);
@@ -203,7 +203,7 @@ qmm_status qmm_kv_create(int32_t type, int64_t n_pages, int32_t page_size, int32
         }
         c->ws = static_cast<float *>(p);
         c->tickets = reinterpret_cast<unsigned *>(static_cast<uint8_t *>(p) + c->ws_bytes);
-        c->status = c->tickets + c->max_blocks;
+        c->status = c->tickets + 3 * c->max_blocks;
         e = cudaMemset(c->tickets, 0, words * 4);
         if (e == cudaSuccess)
             e = cudaStreamSynchronize(nullptr);  // zeroed before a call on any stream

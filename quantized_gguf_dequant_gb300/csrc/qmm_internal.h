@@ -412,7 +412,7 @@ struct KvCache {
     int device = 0, sm_count = 0;
     float *ws = nullptr;  // attention partials: two per block
     size_t ws_bytes = 0;
-    unsigned *tickets = nullptr;  // one per block
+    unsigned *tickets = nullptr;  // three per block, zero between calls
     unsigned *status = nullptr;
     int max_blocks = 0;
 };
