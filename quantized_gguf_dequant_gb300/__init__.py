@@ -359,25 +359,52 @@ class Matrix:
 
 # ------------------------------------------------- the decode step around the products
 
-_DTYPES = {}  # torch dtype -> plain type id, filled on first use
+# These calls are small next to what Python spends on them: checks are plain
+# attribute reads, and what they need of torch and of the library is looked up
+# once (_ops).
+class _Ops:
+    """torch, its dtypes, and the C entries, looked up on first use."""
 
-
-def _dtype(t) -> int:
-    if not _DTYPES:
+    def __init__(self):
         import torch
-        _DTYPES.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
-    try:
-        return _DTYPES[t.dtype]
-    except KeyError:
-        raise ValueError(f"{t.dtype} is not supported (float32, float16 and bfloat16 are)") from None
+        L = lib()
+        self.torch, self.empty = torch, torch.empty
+        self.f32, self.i32, self.i64 = torch.float32, torch.int32, torch.int64
+        self.ids = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+        self.append, self.read, self.attn = L.qmm_kv_append, L.qmm_kv_read, L.qmm_attn_decode
+        self.logits = L.qmm_logits_adjust
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+    def type_id(self, dtype) -> int:
+        n = self.ids.get(dtype)
+        if n is None:
+            raise ValueError(f"{dtype} is not supported (float32, float16 and bfloat16 are)")
+        return n
+
+    def stream(self, stream, device):
+        if stream is None:
+            if self.raw_stream is not None:
+                return self.raw_stream(device)
+            stream = self.torch.cuda.current_stream(device)
+        return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _flat(t, name: str, dtype: str, n=None):
-    """The pointer of a contiguous device tensor of the named dtype (and, with
-    n given, of n elements); None stays None."""
+_the_ops = None
+
+
+def _ops() -> _Ops:
+    global _the_ops
+    if _the_ops is None:
+        _the_ops = _Ops()
+    return _the_ops
+
+
+def _flat(t, name: str, dtype, n=None):
+    """The pointer of a contiguous device tensor of a torch dtype (and, with n
+    given, of n elements); None stays None."""
     if t is None:
         return None
-    if str(t.dtype) != "torch." + dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor on the CUDA device")
@@ -386,28 +413,28 @@ def _flat(t, name: str, dtype: str, n=None):
     return t.data_ptr()
 
 
-def _heads(t, name: str, T: int, heads: int, D: int, dtype=None):
-    """(pointer, elements between tokens) of a [T, heads, D] tensor whose
-    tokens may lie apart, such as a slice of a fused projection's output."""
-    if t.dim() != 3 or tuple(t.shape) != (T, heads, D):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}; {(T, heads, D)} is needed")
-    if dtype is not None and t.dtype != dtype:
+def _heads(t, name: str, shape, dtype):
+    """Elements between the tokens of a [T, heads, D] tensor whose tokens may
+    lie apart, such as a slice of a fused projection's output."""
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; {tuple(shape)} is needed")
+    if t.dtype is not dtype:
         raise ValueError(f"{name} is {t.dtype}; {dtype} is needed")
     if not t.is_cuda:
         raise ValueError(f"{name} must live on the CUDA device")
-    s = t.stride()
-    if s[2] != 1 or (heads > 1 and s[1] != D):
+    T, heads, D = shape
+    a, b, c = t.stride()
+    if c != 1 or (b != D and heads > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), (s[0] if T > 1 else heads * D)
+    return a if T > 1 else heads * D
 
 
 def _made_on(stream, *tensors):
     """Outputs allocated here for work on a stream that is not the current one
     must not return to the allocator before that work is done."""
-    if stream is not None and not isinstance(stream, int):
+    if not isinstance(stream, int):
         for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+            t.record_stream(stream)
 
 
 class Rope:
@@ -426,7 +453,8 @@ class Rope:
         self.n_axes = len(sections)
         self.desc = RopeDesc(2 * n, int(pairing == "adjacent"), len(sections),
                              (ctypes.c_int32 * 4)(*sections),
-                             _flat(inv_freq, "inv_freq", "float32"))
+                             _flat(inv_freq, "inv_freq", _ops().f32))
+        self.ref = ctypes.byref(self.desc)
 
 
 class KVCache:
@@ -453,6 +481,9 @@ class KVCache:
         _check(lib().qmm_kv_create(kind, n_pages, page_size, n_kv_heads, head_dim, _ptr(k),
                                    _ptr(v), ctypes.byref(h)))
         self.h = h.value
+        self._ops, self._device = _ops(), k.device.index or 0
+        self._desc = AttnDesc()  # filled anew by each call (a handle serves one stream)
+        self._desc_ref = ctypes.byref(self._desc)
 
     def close(self):
         if getattr(self, "h", None):
@@ -469,26 +500,32 @@ class KVCache:
         """qmm_kv_append: rotate q and k ([T, heads, head_dim]) and store k and
         v at slots ([T] int64).  pos: [n_axes, T] (or [T]) int32.  Returns the
         rotated q (into q_out, which may be q), or None without q."""
-        import torch
-        T, H, D = k.shape[0], self.n_kv_heads, self.head_dim
-        kp, ldk = _heads(k, "k", T, H, D)
-        vp, ldv = _heads(v, "v", T, H, D, k.dtype)
-        sp = _flat(slots, "slots", "int64", T)
-        qp = qop = None
+        o, D, dtype = self._ops, self.head_dim, k.dtype
+        T = k.shape[0]
+        shape = (T, self.n_kv_heads, D)
+        ldk, ldv = _heads(k, "k", shape, dtype), _heads(v, "v", shape, dtype)
+        qp = qop = pp = desc = None
         ldq = ldqo = n_q = 0
         if q is not None:
             n_q = q.shape[1]
+            shape = (T, n_q, D)
+            ldq = _heads(q, "q", shape, dtype)
             if q_out is None:
-                q_out = torch.empty((T, n_q, D), dtype=q.dtype, device=q.device)
-                _made_on(stream, q_out)
-            qp, ldq = _heads(q, "q", T, n_q, D, k.dtype)
-            qop, ldqo = _heads(q_out, "q_out", T, n_q, D, k.dtype)
-        pp = desc = None
+                q_out = o.empty(shape, dtype=dtype, device=q.device)
+                ldqo = n_q * D
+                if stream is not None:
+                    _made_on(stream, q_out)
+            else:
+                ldqo = _heads(q_out, "q_out", shape, dtype)
+            qp, qop = q.data_ptr(), q_out.data_ptr()
         if rope is not None:
-            pp = _flat(pos, "pos", "int32", rope.n_axes * T)
-            desc = ctypes.byref(rope.desc)
-        _check(lib().qmm_kv_append(self.h, _dtype(k), T, kp, ldk, vp, ldv, sp, qp, ldq, n_q, qop,
-                                   ldqo, pp, desc, _stream(stream)))
+            pp = _flat(pos, "pos", o.i32, rope.n_axes * T)
+            desc = rope.ref
+        rc = o.append(self.h, o.type_id(dtype), T, k.data_ptr(), ldk, v.data_ptr(), ldv,
+                      _flat(slots, "slots", o.i64, T), qp, ldq, n_q, qop, ldqo, pp, desc,
+                      o.stream(stream, self._device))
+        if rc:
+            _check(rc)
         return q_out if q is not None else None
 
     def attend(self, q, page_table, lens, scale=None, softcap: float = 0.0, window: int = 0,
@@ -497,52 +534,68 @@ class KVCache:
         [n_seqs, n_q_heads, head_dim]; page_table: [n_seqs, pages] int32; lens:
         [n_seqs] int32; scale: 1/sqrt(head_dim) by default.  Returns out (like
         q), and with return_lse also lse ([n_seqs, n_q_heads] float32)."""
-        import torch
-        if q.dim() != 3:
-            raise ValueError(f"q has shape {tuple(q.shape)}; [n_seqs, heads, head_dim] is needed")
-        B, n_q, D = q.shape
-        qp, ldq = _heads(q, "q", B, n_q, self.head_dim)
+        o = self._ops
+        shape, dtype = q.shape, q.dtype
+        if len(shape) != 3 or shape[2] != self.head_dim:
+            raise ValueError(f"q has shape {tuple(shape)}; [n_seqs, heads, {self.head_dim}] is needed")
+        B, n_q, D = shape
+        ldq = _heads(q, "q", shape, dtype)
         if out is None:
-            out = torch.empty((B, n_q, D), dtype=q.dtype, device=q.device)
-            _made_on(stream, out)
-        op, ldo = _heads(out, "out", B, n_q, D, q.dtype)
-        if return_lse and lse is None:
-            lse = torch.empty((B, n_q), dtype=torch.float32, device=q.device)
-            _made_on(stream, lse)
-        if page_table.dim() != 2 or page_table.shape[0] != B or page_table.stride(1) != 1 and \
-                page_table.shape[1] > 1:
-            raise ValueError(f"page_table must be [{B}, pages] with contiguous rows")
-        if page_table.dtype != torch.int32 or not page_table.is_cuda:
+            out = o.empty(shape, dtype=dtype, device=q.device)
+            ldo = n_q * D
+            if stream is not None:
+                _made_on(stream, out)
+        else:
+            ldo = _heads(out, "out", shape, dtype)
+        lp = None
+        if lse is not None:
+            lp = _flat(lse, "lse", o.f32, B * n_q)
+        elif return_lse:
+            lse = o.empty((B, n_q), dtype=o.f32, device=q.device)
+            lp = lse.data_ptr()
+            if stream is not None:
+                _made_on(stream, lse)
+        if page_table.dim() != 2 or page_table.shape[0] != B:
+            raise ValueError(f"page_table must be [{B}, pages]")
+        if page_table.dtype is not o.i32 or not page_table.is_cuda:
             raise ValueError("page_table must be int32 on the CUDA device")
-        width = page_table.shape[1]
-        if B > 1 and page_table.stride(0) != width:
-            page_table = page_table.contiguous()  # (the ABI takes a row's length as its stride)
-            _made_on(stream, page_table)
-        if scale is None:
-            scale = D ** -0.5
-        desc = AttnDesc(scale, softcap, window, _flat(alibi, "alibi", "float32", n_q))
-        _check(lib().qmm_attn_decode(self.h, _dtype(q), B, n_q, qp, ldq, page_table.data_ptr(),
-                                     width, _flat(lens, "lens", "int32", B), ctypes.byref(desc),
-                                     op, ldo, _flat(lse, "lse", "float32", B * n_q),
-                                     _stream(stream)))
+        if not page_table.is_contiguous():  # (the ABI takes a row's length as its stride)
+            raise ValueError("page_table must be contiguous")
+        d = self._desc
+        d.scale = D ** -0.5 if scale is None else scale
+        d.softcap, d.window = softcap, window
+        d.alibi = None if alibi is None else _flat(alibi, "alibi", o.f32, n_q)
+        rc = o.attn(self.h, o.type_id(dtype), B, n_q, q.data_ptr(), ldq, page_table.data_ptr(),
+                    page_table.shape[1], _flat(lens, "lens", o.i32, B), self._desc_ref,
+                    out.data_ptr(), ldo, lp, o.stream(stream, self._device))
+        if rc:
+            _check(rc)
         return (out, lse) if return_lse else out
 
     def read(self, slots, dtype=None, k_out=None, v_out=None, stream=None):
         """qmm_kv_read: (k, v) values of the slots, [T, n_kv_heads, head_dim]."""
-        import torch
-        T, H, D = slots.numel(), self.n_kv_heads, self.head_dim
-        dtype = dtype or (k_out.dtype if k_out is not None else torch.float32)
-        made = []
-        for given in (k_out, v_out):
-            if given is None:
-                given = torch.empty((T, H, D), dtype=dtype, device=slots.device)
-                _made_on(stream, given)
-            made.append(given)
-        kp, ldk = _heads(made[0], "k_out", T, H, D, dtype)
-        vp, ldv = _heads(made[1], "v_out", T, H, D, dtype)
-        _check(lib().qmm_kv_read(self.h, _dtype(made[0]), T, _flat(slots, "slots", "int64"), kp,
-                                 ldk, vp, ldv, _stream(stream)))
-        return made[0], made[1]
+        o = self._ops
+        T, D = slots.numel(), self.head_dim
+        shape = (T, self.n_kv_heads, D)
+        dtype = dtype or (k_out.dtype if k_out is not None else o.f32)
+        ldk = ldv = self.n_kv_heads * D
+        if k_out is None:
+            k_out = o.empty(shape, dtype=dtype, device=slots.device)
+            if stream is not None:
+                _made_on(stream, k_out)
+        else:
+            ldk = _heads(k_out, "k_out", shape, dtype)
+        if v_out is None:
+            v_out = o.empty(shape, dtype=dtype, device=slots.device)
+            if stream is not None:
+                _made_on(stream, v_out)
+        else:
+            ldv = _heads(v_out, "v_out", shape, dtype)
+        rc = o.read(self.h, o.type_id(dtype), T, _flat(slots, "slots", o.i64), k_out.data_ptr(),
+                    ldk, v_out.data_ptr(), ldv, o.stream(stream, self._device))
+        if rc:
+            _check(rc)
+        return k_out, v_out
 
     def status(self) -> int:
         """The handle's device status (0 = OK); clears it."""
@@ -564,40 +617,55 @@ def logits_adjust(logits, out=None, *, history=None, history_offsets=None, repea
     one row of) logits.  history, bias_ids: int32, ragged by the rows + 1 int64
     offsets; repeat, presence, frequency: float32 [rows]; mask: int32 words
     [rows, words], or one row [words] for all.  out may be logits."""
-    import torch
-    if logits.dim() not in (1, 2) or not logits.is_cuda or \
-            (logits.shape[-1] > 1 and logits.stride(-1) != 1):
+    o = _ops()
+    shape, dtype, stride = logits.shape, logits.dtype, logits.stride()
+    if len(shape) not in (1, 2) or not logits.is_cuda or (stride[-1] != 1 and shape[-1] > 1):
         raise ValueError("logits must be [rows, vocabulary] or [vocabulary] on the CUDA device, "
                          "each row contiguous")
+    B, V = shape if len(shape) == 2 else (1, shape[0])
+    ld = ldo = V
     if out is None:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-        _made_on(stream, out)
-    if out.shape != logits.shape or out.dtype != logits.dtype or not out.is_cuda or \
-            (out.shape[-1] > 1 and out.stride(-1) != 1):
-        raise ValueError("out must be like logits")
-    B, V = (1, logits.shape[0]) if logits.dim() == 1 else logits.shape
-    ld, ldo = (logits.stride(0), out.stride(0)) if logits.dim() == 2 and B > 1 else (V, V)
+        out = o.empty(shape, dtype=dtype, device=logits.device)
+        if stream is not None:
+            _made_on(stream, out)
+    else:
+        if out.shape != shape or out.dtype is not dtype or not out.is_cuda or \
+                (out.stride(-1) != 1 and V > 1):
+            raise ValueError("out must be like logits")
+        if B > 1:
+            ldo = out.stride(0)
+    if B > 1:
+        ld = stride[0]
     r = LogitRules()
-    if history is not None and history.numel():
-        r.history = _flat(history, "history", "int32")
-        r.history_offsets = _flat(history_offsets, "history_offsets", "int64", B + 1)
-        r.n_history = history.numel()
-    r.repeat = _flat(repeat, "repeat", "float32", B)
-    r.presence = _flat(presence, "presence", "float32", B)
-    r.frequency = _flat(frequency, "frequency", "float32", B)
-    if bias_ids is not None and bias_ids.numel():
+    f32, i32, i64 = o.f32, o.i32, o.i64
+    if history is not None:
+        n = history.numel()
+        if n:
+            r.history = _flat(history, "history", i32)
+            r.history_offsets = _flat(history_offsets, "history_offsets", i64, B + 1)
+            r.n_history = n
+    if repeat is not None:
+        r.repeat = _flat(repeat, "repeat", f32, B)
+    if presence is not None:
+        r.presence = _flat(presence, "presence", f32, B)
+    if frequency is not None:
+        r.frequency = _flat(frequency, "frequency", f32, B)
+    if bias_ids is not None:
         n = bias_ids.numel()
-        r.bias_ids = _flat(bias_ids, "bias_ids", "int32")
-        r.bias_values = _flat(bias_values, "bias_values", "float32", n)
-        r.bias_offsets = _flat(bias_offsets, "bias_offsets", "int64", B + 1)
-        r.n_biases = n
+        if n:
+            r.bias_ids = _flat(bias_ids, "bias_ids", i32)
+            r.bias_values = _flat(bias_values, "bias_values", f32, n)
+            r.bias_offsets = _flat(bias_offsets, "bias_offsets", i64, B + 1)
+            r.n_biases = n
     if mask is not None:
-        words = mask.shape[-1]
-        if words * 32 < V or mask.numel() not in (words, B * words):
+        words, n = mask.shape[-1], mask.numel()
+        if words * 32 < V or (n != words and n != B * words):
             raise ValueError(f"mask of shape {tuple(mask.shape)} does not hold {B} or 1 rows of "
                              f"{V} bits")
-        r.mask = _flat(mask, "mask", "int32")
-        r.ld_mask = words if mask.numel() == B * words else 0
-    _check(lib().qmm_logits_adjust(_dtype(logits), B, V, logits.data_ptr(), ld, ctypes.byref(r),
-                                   out.data_ptr(), ldo, _stream(stream)))
+        r.mask = _flat(mask, "mask", i32)
+        r.ld_mask = words if n == B * words else 0
+    rc = o.logits(o.type_id(dtype), B, V, logits.data_ptr(), ld, ctypes.byref(r), out.data_ptr(),
+                  ldo, o.stream(stream, logits.device.index))
+    if rc:
+        _check(rc)
     return out

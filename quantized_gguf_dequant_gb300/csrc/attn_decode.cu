@@ -1,1035 +1,16 @@
-// attn_decode.cu -- attention of one new token per sequence over the paged
-// key-value cache, split over the cache's length and joined.
-//
-//   s_j = scale q.k_j;  capped: cap tanh(s/cap);  + slope_h (j - (len-1))
-//   out = sum_j softmax(s)_j v_j,  lse = ln sum_j exp(s_j),
-//   j over the keys in [max(0, len - window), len)
-//
-// One pass over the cache with a running maximum m and sum l (base 2):
-// a tile of 16 keys rescales what was gathered by 2^(m_old - m_new).
-//
-// What bounds it: the cache bytes.  Every key and value is read once for the
-// up to eight query heads that share it and used for 4 flops a head, far
-// below what the tensor cores take, so the design is about keeping enough
-// loads in flight.  Each of a block's four warps streams its own 16-key tiles
-// through its own ring of shared-memory stages with cp.async (no block-wide
-// barrier inside a segment; masked keys are not read but filled with zeros,
-// so that stale NaNs cannot meet a zero probability).
-//
-// Split: the 16-key tiles of all (sequence, kv head, eight query heads) items
-// form one list, cut into equal contiguous ranges, one per resident block,
-// whatever the lengths; the lengths are read on the device, so a captured
-// graph serves every step.  An item that spans blocks leaves one partial
-// (m, l, sum) per block in the workspace; the block that finishes last
-// (a ticket per item) joins them in block order, so results are bitwise
-// repeatable.
-//
-// Products run on mma.sync m16n8k16 (two operands of 16 bits, fp32 sums): at
-// one new token the tensor work is a fraction of the load time, and eight
-// heads fill its n (values) or half its m (keys).  Activations stay in fp32
-// precision: q is split into 16-bit pieces whose sum is q to 22 bits or more
-// (two pieces after a power-of-two normalisation for f16 operands, three for
-// bf16), and so are the probabilities.  The first two q pieces share one
-// instruction: piece 0 in rows 0-7, piece 1 in rows 8-15.
-//   QK:  S[16 = (piece, head)][8 keys] += Q[16][16 d] K[8 keys][16 d]^T
-//   PV:  O^T[16 d][8 heads] = V[16 keys][16 d]^T P[16 keys][8 heads]
-// The score registers of a tile are the value product's B operand as they
-// stand.  The value product of a tile starts from zero and is added to the
-// running sum with a rounding FMA: sums kept inside the tensor cores lose
-// low bits over thousands of tiles.
-// Q8_0: codes become f16 exactly (a byte permute and a subtract); key scales
-// multiply the scores of their 32-value block, value scales the
-// probabilities, which are first brought to f16's range by the power of two
-// that the largest value scale so far asks for.
-#include <algorithm>
-#include <cfloat>
+// attn_decode.cu -- which of the decode attention's kernels (attn_kernel.cuh) runs.
 #include <cstring>
-#include <type_traits>
 
-#include "kv_cache.cuh"
-#include "qmm_device.cuh"
 #include "qmm_internal.h"
 
 namespace qmm {
-
-namespace {
-
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kTile = 16;  // keys per tile (the instruction's k and two n)
-constexpr int kH = kAttnHeads;
-constexpr int kLens = 512;  // lengths kept in shared memory
-// The fixed part of an item's time in a block (its first loads, its joins), in
-// the time of 16-key tiles; blocks get equal shares of tiles and these.
-constexpr int kItemCost = 12;
-// A block takes at least so much: splitting an item costs a join, which is
-// worth it from about twenty saved tiles on.
-constexpr int kMinUnits = 36;
-constexpr int kStatic = 2560;  // the kernel's static shared memory, at most
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-enum Kind { kF16, kBF16, kQ8 };
-
-struct AttnParams {
-    AttnArgs a;
-    int group;          // query heads per kv head
-    int head_tiles;     // ceil(group / 8)
-    int items;          // kv heads * head tiles
-    int min_units;      // units (16-key tiles, and kItemCost an item) a block takes at least
-};
-
-template <Kind KIND, int D>
-struct Shape {
-    static constexpr int ROWB = KIND == kQ8 ? D : 2 * D;           // bytes of a row
-    // Rows in shared memory: 16-byte chunk c of row r sits at c ^ (r & 7) where
-    // rows are whole 128 bytes, else rows are padded by 16 bytes; either way the
-    // eight rows of an ldmatrix lie in different banks.  Q8_0 rows of 32 or 96
-    // mod 128 bytes spread its 8-byte loads.
-    static constexpr bool SWZ = KIND != kQ8 && D % 64 == 0;
-    static constexpr int RS = KIND == kQ8 ? ROWB + (D % 64 == 0 ? 32 : 0) : ROWB + (SWZ ? 0 : 16);
-    static constexpr int SP = kv_scales_per_row(D);
-    static constexpr int SCB = KIND == kQ8 ? SP * 2 : 0;           // bytes of a row's scales
-    static constexpr int STAGE = 2 * kTile * (RS + SCB);
-    static constexpr int CHUNKS = ROWB / 16;                       // 16-byte chunks of a row
-    static constexpr int KSTEPS = D / 16;
-    static constexpr int QFRAG = KSTEPS * 512 + (KIND == kBF16 ? KSTEPS * 256 : 0);
-    static constexpr int OSTRIDE = D + 4;
-    static constexpr int JOIN = kWarps * kH * (OSTRIDE + 2) * 4;
-    // Resident blocks an SM: as many as leave two stages a warp (and, for the
-    // registers, four): a warp's work on a tile is a chain of dependent
-    // steps that other warps have to cover.
-    static constexpr int LEAST = QFRAG + 2 * kWarps * STAGE + kStatic + 1024;
-    static constexpr int BLOCKS = 228 * 1024 / LEAST < 4 ? 228 * 1024 / LEAST : 4;
-    static constexpr int FIT =
-        (228 * 1024 / BLOCKS - QFRAG - kStatic - 1024) / (kWarps * STAGE);
-    static constexpr int STAGES = FIT < 6 ? FIT : 6;
-    static constexpr int RING = kWarps * STAGES * STAGE;
-    static constexpr int SMEM = QFRAG + (RING > JOIN ? RING : JOIN);
-    static_assert(STAGES >= 2, "ring");
-    // Address of 16-value column ks of a row, from that of column 0.
-    static __device__ __forceinline__ uint32_t chunk_at(uint32_t row, int ks)
-    {
-        return SWZ ? (row ^ ((ks & 3) * 32)) + (ks >> 2) * 128 : row + ks * 32;
-    }
-};
-
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, unsigned bytes)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ void cp4(uint32_t dst, const void *src, unsigned bytes)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t addr)
-{
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t addr)
-{
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
-    return v;
-}
-
-template <Kind KIND>
-__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                    uint32_t a3, uint32_t b0, uint32_t b1)
-{
-    if constexpr (KIND == kBF16)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-            "{%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-            "{%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-template <Kind KIND>
-using Half = typename std::conditional<KIND == kBF16, __nv_bfloat16, __half>::type;
-
-__device__ __forceinline__ float2 unpack2(uint32_t u, __half)
-{
-    return __half22float2(*reinterpret_cast<const __half2 *>(&u));
-}
-__device__ __forceinline__ float2 unpack2(uint32_t u, __nv_bfloat16)
-{
-    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-}
-
-// Four int8 codes, as bytes code + 128, to two pairs of f16: 1024 + byte by
-// the exponent byte 0x64, minus 1152.
-__device__ __forceinline__ uint32_t codes_f16(uint32_t biased, unsigned sel)
-{
-    const uint32_t w = __byte_perm(biased, 0x64646464u, sel);
-    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&w),
-                              __half2half2(__ushort_as_half(0x6480)));
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-// The tile list of one sequence: keys [lo, hi), tiles t0 .. t0 + n - 1 (in
-// units of 16 keys from key 0).
-struct Span {
-    int lo, hi, t0, n;
-};
-__device__ __forceinline__ Span span_of(const AttnArgs &a, int len)
-{
-    Span s;
-    s.hi = max(0, min(len, int(min(a.ld_table * a.c.page_size, int64_t(0x7fffffe0)))));
-    s.lo = a.window > 0 ? max(0, s.hi - a.window) : 0;
-    s.t0 = s.lo / kTile;
-    s.n = s.hi > s.lo ? (s.hi + kTile - 1) / kTile - s.t0 : 0;
-    return s;
-}
-
-template <typename IO>
-__device__ __forceinline__ float load_io(const void *p, int64_t i)
-{
-    return load1(static_cast<const IO *>(p) + i);
-}
-__device__ __forceinline__ float load_any(const void *p, int64_t i, int dtype)
-{
-    return dtype == QMM_F32   ? load_io<float>(p, i)
-           : dtype == QMM_F16 ? load_io<__half>(p, i)
-                              : load_io<__nv_bfloat16>(p, i);
-}
-__device__ __forceinline__ void store4_any(void *p, int64_t i, float4 v, int dtype)
-{
-    if (dtype == QMM_F32)
-        store4(static_cast<float *>(p) + i, v);
-    else if (dtype == QMM_F16)
-        store4(static_cast<__half *>(p) + i, v);
-    else
-        store4(static_cast<__nv_bfloat16 *>(p) + i, v);
-}
-__device__ __forceinline__ void add4(float4 &s, float f, float4 v)
-{
-    s.x += f * v.x;
-    s.y += f * v.y;
-    s.z += f * v.z;
-    s.w += f * v.w;
-}
-
-// The dim of a head that lane group g's accumulator pair x of value tile ds holds.
-template <Kind KIND>
-__device__ __forceinline__ int dim_of(int ds, int g, int x)
-{
-    return KIND == kQ8 ? (ds / 2) * 32 + 4 * g + 2 * (ds & 1) + x : ds * 16 + g + x * 8;
-}
-
-// One value of a buffer (data, and the scales of Q8_0): the slow paths' access.
-template <Kind KIND, int D>
-__device__ __forceinline__ float value_at(const uint8_t *data, const void *scales, uint64_t row,
-                                          int d)
-{
-    if constexpr (KIND == kQ8)
-        return float(reinterpret_cast<const int8_t *>(data)[row * D + d]) *
-               __half2float(static_cast<const __half *>(scales)[row * kv_scales_per_row(D) + d / 32]);
-    else
-        return load1(reinterpret_cast<const Half<KIND> *>(data) + row * D + d);
-}
-
-template <Kind KIND, int D>
-__global__ void __launch_bounds__(kThreads, Shape<KIND, D>::BLOCKS) attn_kernel(const __grid_constant__ AttnParams P)
-{
-    using S = Shape<KIND, D>;
-    using H = Half<KIND>;
-    constexpr int STAGES = S::STAGES;
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t warp_units[kWarps];
-    __shared__ int64_t found_at;   // first tile of the sequence that the block starts in
-    __shared__ int found_seq;
-    __shared__ int lens[kLens];
-    __shared__ unsigned valid_ring[kWarps][STAGES];
-    __shared__ int qexp[kH];
-    __shared__ bool qfinite[kH];
-    __shared__ bool last_block;
-
-    const AttnArgs &A = P.a;
-    const KvView &C = A.c;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int g = lane >> 2, t = lane & 3;
-    pdl_wait();
-    pdl_launch_dependents();
-
-    // ---- the plan: prefix sums of the sequences' tiles
-    for (int b = tid; b < min(A.n_seqs, kLens); b += kThreads)
-        lens[b] = __ldg(A.lens + b);
-    __syncthreads();
-    auto units_of = [&](int n) { return n ? int64_t(n + kItemCost) * P.items : int64_t(0); };
-    auto len_of = [&](int b) { return b < kLens ? lens[b] : __ldg(A.lens + b); };
-    const int per_thread = (A.n_seqs + kThreads - 1) / kThreads;
-    const int sb0 = min(A.n_seqs, tid * per_thread), sb1 = min(A.n_seqs, sb0 + per_thread);
-    int64_t mine = 0;
-    for (int b = sb0; b < sb1; ++b) {
-        const int len = len_of(b);
-        const Span sp = span_of(A, len);
-        mine += units_of(sp.n);
-        if (blockIdx.x == 0 && (len < 0 || len > sp.hi))
-            atomicOr(A.status, kStatusBadLengthBit);
-    }
-    // sequences without keys are no one's item: their outputs are zero
-    for (int b = blockIdx.x; b < A.n_seqs; b += gridDim.x) {
-        if (span_of(A, len_of(b)).n > 0)
-            continue;
-        for (int i = tid; i < A.n_q * D / 4; i += kThreads)
-            store4_any(A.out, b * A.ldo + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f), A.dtype);
-        if (A.lse)
-            for (int i = tid; i < A.n_q; i += kThreads)
-                A.lse[int64_t(b) * A.n_q + i] = -INFINITY;
-    }
-    int64_t upto = mine;  // units of the sequences up to this thread's
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-        upto += lane >= o ? v : 0;
-    }
-    if (lane == 31)
-        warp_units[warp] = upto;
-    __syncthreads();
-    int64_t total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        upto += w < warp ? warp_units[w] : 0;
-        total += warp_units[w];
-    }
-    if (total == 0)
-        return;
-    // block c takes units [c * per, (c + 1) * per): unit x is block x / per's
-    const int64_t per = max(int64_t(P.min_units),
-                            int64_t((uint64_t(total) + gridDim.x - 1) / gridDim.x));
-    const int64_t blk = blockIdx.x, r0 = per * blk, r1 = min(total, r0 + per);
-    if (r0 >= total)
-        return;
-    if (r0 < upto && r0 >= upto - mine) {
-        int64_t at = upto - mine;
-        for (int b = sb0; b < sb1; ++b) {
-            const int64_t n = units_of(span_of(A, len_of(b)).n);
-            if (r0 < at + n) {
-                found_seq = b;
-                found_at = at;
-                break;
-            }
-            at += n;
-        }
-    }
-    __syncthreads();
-    int seq = found_seq;
-    int64_t seq_at = found_at;
-    Span sp = span_of(A, len_of(seq));
-
-    const uint32_t smem_base = smem_u32(smem);
-    // this lane's row and half-chunk of an ldmatrix over 16 keys x 16 values
-    const uint32_t frag_row =
-        ((lane >> 4) * 8 + (lane & 7)) * S::RS +
-        (S::SWZ ? ((lane >> 3) & 1) ^ (lane & 7) : (lane >> 3) & 1) * 16;
-    const uint32_t ring = smem_base + S::QFRAG + warp * STAGES * S::STAGE;
-    float *join = reinterpret_cast<float *>(smem + S::QFRAG);
-    float *join_ml = join + kWarps * kH * S::OSTRIDE;
-
-    for (int64_t at = r0; at < r1;) {
-        while (at >= seq_at + units_of(sp.n)) {
-            seq_at += units_of(sp.n);
-            ++seq;
-            sp = span_of(A, len_of(seq));
-        }
-        // the item and this block's tiles [ta, tb) of it
-        const int item = int(uint64_t(at - seq_at) / unsigned(sp.n + kItemCost));
-        const int64_t tiles_at = seq_at + int64_t(item) * (sp.n + kItemCost) + kItemCost;
-        const int ta = int(max(int64_t(0), at - tiles_at));
-        const int tb = int(max(int64_t(0), min(r1 - tiles_at, int64_t(sp.n))));
-        at = tiles_at + sp.n;
-        if (tb <= ta)
-            break;  // the range ends in the item's overhead: the next block starts the item
-        const int kvh = item / P.head_tiles, h0 = (item % P.head_tiles) * kH;
-        const int nh = min(kH, P.group - h0);
-        const int head0 = kvh * P.group + h0;  // first query head
-        const int nw = max(0, (tb - ta - warp + kWarps - 1) / kWarps);  // this warp's tiles
-        const int32_t *table = A.table + int64_t(seq) * A.ld_table;
-
-        // ---- loading
-        auto key_of = [&](int i) { return (sp.t0 + ta + warp + i * kWarps) * kTile + (lane & 15); };
-        // the page of this lane's key of tile i (a guarded load and no branch,
-        // so that several are under way at once)
-        auto page_id = [&](int i) -> int {
-            const int j = key_of(i);
-            const bool in = i < nw && j >= sp.lo && j < sp.hi;
-            const int id = __ldg(table + (in ? fast_div(C.page, unsigned(j)) : 0u));
-            return in ? id : -1;
-        };
-        auto row_of = [&](int j, uint32_t &row) {  // (the slow paths')
-            if (j < sp.lo || j >= sp.hi)
-                return false;
-            const unsigned pg = fast_div(C.page, unsigned(j));
-            const int id = __ldg(table + pg);
-            row = (uint32_t(id) * unsigned(C.n_heads) + unsigned(kvh)) * C.page.d + unsigned(j) -
-                  pg * C.page.d;
-            return unsigned(id) < C.n_pages;
-        };
-        auto issue = [&](int i, int id) {
-            if (i < nw) {
-                const int j = key_of(i);
-                const bool ok = unsigned(id) < C.n_pages;
-                if (!ok && j >= sp.lo && j < sp.hi)
-                    atomicOr(A.status, kStatusBadPageBit);
-                uint32_t row = 0;
-                if (ok) {
-                    const uint32_t off = unsigned(j) - fast_div(C.page, unsigned(j)) * C.page.d;
-                    row = (uint32_t(id) * unsigned(C.n_heads) + unsigned(kvh)) * C.page.d + off;
-                }
-                const unsigned valid = __ballot_sync(0xffffffffu, ok) & 0xffffu;
-                const int st = i % STAGES;
-                if (lane == 0)
-                    valid_ring[warp][st] = valid;
-                const uint32_t kdst = ring + st * S::STAGE, vdst = kdst + kTile * S::RS;
-#pragma unroll
-                for (int it = 0; it < kTile * S::CHUNKS / 32; ++it) {
-                    const int idx = it * 32 + lane;
-                    const int r = idx / S::CHUNKS, ch = idx % S::CHUNKS;
-                    const uint64_t o =
-                        uint64_t(__shfl_sync(0xffffffffu, row, r)) * S::ROWB + ch * 16;
-                    const unsigned bytes = (valid >> r) & 1u ? 16u : 0u;
-                    const unsigned at = r * S::RS + (S::SWZ ? ch ^ (r & 7) : ch) * 16;
-                    cp16(kdst + at, C.k + o, bytes);
-                    cp16(vdst + at, C.v + o, bytes);
-                }
-                if constexpr (KIND == kQ8) {
-                    constexpr int W = S::SCB / 4;  // words of a row's scales
-                    const uint32_t sdst = kdst + 2 * kTile * S::RS;
-#pragma unroll
-                    for (int it = 0; it < (kTile * W + 31) / 32; ++it) {
-                        const int idx = it * 32 + lane;
-                        const int r = (idx / W) & 15, w = idx % W;
-                        const uint64_t o =
-                            uint64_t(__shfl_sync(0xffffffffu, row, r)) * S::SCB + w * 4;
-                        const unsigned bytes = (valid >> r) & 1u ? 4u : 0u;
-                        if (idx < kTile * W) {
-                            cp4(sdst + idx * 4, static_cast<const uint8_t *>(C.ks) + o, bytes);
-                            cp4(sdst + kTile * S::SCB + idx * 4,
-                                static_cast<const uint8_t *>(C.vs) + o, bytes);
-                        }
-                    }
-                }
-            }
-            cp_commit();
-        };
-        // q of head tid/16, issued ahead of everything that waits
-        float qv[D / 16];
-        {
-            const int h = tid >> 4;
-            const int64_t q0 =
-                int64_t(seq) * A.ldq + int64_t(head0 + min(h, nh - 1)) * D + (tid & 15);
-            if (A.dtype == QMM_F32) {
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i)
-                    qv[i] = __ldg(static_cast<const float *>(A.q) + q0 + i * 16);
-            } else if (A.dtype == QMM_F16) {
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i)
-                    qv[i] = load_io<__half>(A.q, q0 + i * 16);
-            } else {
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i)
-                    qv[i] = load_io<__nv_bfloat16>(A.q, q0 + i * 16);
-            }
-        }
-        int next_id;
-        {
-            int ids[STAGES];
-#pragma unroll
-            for (int i = 0; i < STAGES; ++i)
-                ids[i] = page_id(i);
-#pragma unroll
-            for (int i = 0; i < STAGES - 1; ++i)
-                issue(i, ids[i]);
-            next_id = ids[STAGES - 1];
-        }
-
-        // ---- q's pieces as A operands, by 16 threads a head
-        {
-            const int h = tid >> 4, lt = tid & 15;
-            float mx = 0.f, sum = 0.f;  // sum: 0, or NaN where q is not finite
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                qv[i] = h < nh ? qv[i] : 0.f;
-                mx = fmaxf(mx, fabsf(qv[i]));
-                sum += qv[i] * 0.f;
-            }
-            int e = 0;
-#pragma unroll
-            for (int o = 1; o < 16; o <<= 1) {
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            }
-            if constexpr (KIND != kBF16) {
-                // the largest component to [2^13, 2^14)
-                e = max(-126, min(126, 13 - (int(__float_as_uint(mx) >> 23) - 127)));
-            }
-            if (lt == 0) {
-                qexp[h] = e;
-                qfinite[h] = sum == 0.f;
-            }
-            uint16_t *frag = reinterpret_cast<uint16_t *>(smem);
-            uint16_t *frag3 = reinterpret_cast<uint16_t *>(smem + S::KSTEPS * 512);
-            const float f = exp2i(e);
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                const int d = i * 16 + lt;
-                int ks, ln, hi, lo;
-                if constexpr (KIND == kQ8) {
-                    // lane t of a key holds codes 8t .. 8t+7 of a 32-block
-                    const int in = d & 31;
-                    ks = (d >> 5) * 2 + ((in >> 2) & 1);
-                    ln = h * 4 + (in >> 3);
-                    hi = (in >> 1) & 1;
-                    lo = in & 1;
-                } else {
-                    const int in = d & 15;
-                    ks = d >> 4;
-                    ln = h * 4 + ((in & 7) >> 1);
-                    hi = in >> 3;
-                    lo = in & 1;
-                }
-                const float x = qv[i] * f;
-                const H p0 = H(x);
-                const float r1 = x - float(p0);
-                const H p1 = H(r1);
-                const int w = (ks * 32 + ln) * 8 + lo;  // 16-bit units; registers are 2 apart
-                frag[w + (2 * hi) * 2] = *reinterpret_cast<const uint16_t *>(&p0);
-                frag[w + (2 * hi + 1) * 2] = *reinterpret_cast<const uint16_t *>(&p1);
-                if constexpr (KIND == kBF16) {
-                    const H p2 = H(r1 - float(p1));
-                    frag3[(ks * 32 + ln) * 4 + hi * 2 + lo] =
-                        *reinterpret_cast<const uint16_t *>(&p2);
-                }
-            }
-        }
-        __syncthreads();
-
-        const float qscale = A.scale * exp2i(-qexp[g]);
-        const float cap_inv = A.softcap > 0.f ? 1.f / A.softcap : 0.f;
-        const float slope =
-            A.alibi && g < nh ? __ldg(A.alibi + head0 + g) * kLog2e : 0.f;
-        // f16 probabilities are carried 2^14 times as large, clear of its subnormals
-        constexpr float kBias = KIND == kF16 ? 14.f : 0.f;
-        float m = -INFINITY, l = 0.f;  // of head g
-        int vexp = -126;               // Q8_0: exponent of the largest value scale so far
-        float O[D / 16][4] = {};
-
-        for (int i = 0; i < nw; ++i) {
-            issue(i + STAGES - 1, next_id);
-            next_id = page_id(i + STAGES);
-            cp_wait<STAGES - 1>();
-            __syncwarp();
-            const int st = i % STAGES;
-            const uint32_t kb = ring + st * S::STAGE, vb = kb + kTile * S::RS;
-            const uint32_t ksb = vb + kTile * S::RS, vsb = ksb + kTile * S::SCB;
-
-            // ---- scores of head g at keys 2t, 2t+1, 2t+8, 2t+9
-            float s[4];
-            if constexpr (KIND == kQ8) {
-                s[0] = s[1] = s[2] = s[3] = 0.f;
-#pragma unroll
-                for (int blk = 0; blk < D / 32; ++blk) {
-                    float c0[4] = {}, c1[4] = {};
-                    const uint4 a0 = *reinterpret_cast<const uint4 *>(
-                        smem + ((2 * blk) * 32 + lane) * 16);
-                    const uint4 a1 = *reinterpret_cast<const uint4 *>(
-                        smem + ((2 * blk + 1) * 32 + lane) * 16);
-                    uint2 w = lds64(kb + g * S::RS + blk * 32 + t * 8);
-                    w.x ^= 0x80808080u;
-                    w.y ^= 0x80808080u;
-                    mma<KIND>(c0, a0.x, a0.y, a0.z, a0.w, codes_f16(w.x, 0x4140),
-                              codes_f16(w.x, 0x4342));
-                    mma<KIND>(c0, a1.x, a1.y, a1.z, a1.w, codes_f16(w.y, 0x4140),
-                              codes_f16(w.y, 0x4342));
-                    w = lds64(kb + (g + 8) * S::RS + blk * 32 + t * 8);
-                    w.x ^= 0x80808080u;
-                    w.y ^= 0x80808080u;
-                    mma<KIND>(c1, a0.x, a0.y, a0.z, a0.w, codes_f16(w.x, 0x4140),
-                              codes_f16(w.x, 0x4342));
-                    mma<KIND>(c1, a1.x, a1.y, a1.z, a1.w, codes_f16(w.y, 0x4140),
-                              codes_f16(w.y, 0x4342));
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int key = 2 * t + (x & 1) + (x >> 1) * 8;
-                        const __half *sc = reinterpret_cast<const __half *>(
-                            smem + (ksb - smem_base) + key * S::SCB);
-                        const float *cc = x < 2 ? c0 : c1;
-                        s[x] += (cc[x & 1] + cc[2 + (x & 1)]) * __half2float(sc[blk]);
-                    }
-                }
-            } else {
-                float c0[4] = {}, c1[4] = {};
-                const uint32_t kaddr = kb + frag_row;
-                if constexpr (KIND == kBF16) {
-                    // the smallest piece first: its sum is exact next to the others'
-#pragma unroll
-                    for (int ks = 0; ks < S::KSTEPS; ++ks) {
-                        uint32_t b[4];
-                        ldsm4(b, S::chunk_at(kaddr, ks));
-                        const uint2 a3 = *reinterpret_cast<const uint2 *>(
-                            smem + S::KSTEPS * 512 + (ks * 32 + lane) * 8);
-                        mma<KIND>(c0, a3.x, 0u, a3.y, 0u, b[0], b[1]);
-                        mma<KIND>(c1, a3.x, 0u, a3.y, 0u, b[2], b[3]);
-                    }
-                }
-#pragma unroll
-                for (int ks = 0; ks < S::KSTEPS; ++ks) {
-                    uint32_t b[4];
-                    ldsm4(b, S::chunk_at(kaddr, ks));
-                    const uint4 a =
-                        *reinterpret_cast<const uint4 *>(smem + (ks * 32 + lane) * 16);
-                    mma<KIND>(c0, a.x, a.y, a.z, a.w, b[0], b[1]);
-                    mma<KIND>(c1, a.x, a.y, a.z, a.w, b[2], b[3]);
-                }
-                s[0] = c0[0] + c0[2];
-                s[1] = c0[1] + c0[3];
-                s[2] = c1[0] + c1[2];
-                s[3] = c1[1] + c1[3];
-            }
-            const unsigned valid = valid_ring[warp][st];
-            const int key0 = (sp.t0 + ta + warp + i * kWarps) * kTile;
-            // An infinite key component times pieces of q gives NaN where the
-            // product with q itself is infinite: settle it with q itself.
-            const bool odd = qfinite[g] && !(s[0] + s[1] + s[2] + s[3] == s[0] + s[1] + s[2] + s[3]);
-            if (__any_sync(0xffffffffu, odd)) {
-                const int64_t q0 = int64_t(seq) * A.ldq + int64_t(head0 + g) * D;
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    uint32_t row;
-                    if (!qfinite[g] || g >= nh || s[x] == s[x] ||
-                        !row_of(key0 + 2 * t + (x & 1) + (x >> 1) * 8, row))
-                        continue;
-                    float dot = 0.f;
-                    for (int d = 0; d < D; ++d)
-                        dot += load_any(A.q, q0 + d, A.dtype) *
-                               value_at<KIND, D>(C.k, C.ks, row, d);
-                    s[x] = dot * exp2i(qexp[g]);
-                }
-            }
-            float tmax = -INFINITY;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int key = 2 * t + (x & 1) + (x >> 1) * 8;
-                float v = s[x] * qscale;
-                if (A.softcap > 0.f)
-                    v = A.softcap * tanhf(v * cap_inv);
-                v = v * kLog2e + slope * float(key0 + key - (sp.hi - 1));
-                s[x] = (valid >> key) & 1u ? v : -INFINITY;
-                tmax = fmaxf(tmax, s[x]);
-            }
-            tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 1));
-            tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 2));
-            const float mn = fmaxf(m, tmax);
-            const float base = mn == -INFINITY ? 0.f : mn;
-            const float corr = ex2(m - base);  // 0 while nothing was seen
-            m = mn;
-            float p[4], psum = 0.f;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                p[x] = ex2(s[x] - (base - kBias));
-                psum += p[x];
-            }
-            l = l * corr + psum;
-            // O holds heads 2t and 2t+1
-            float f0 = __shfl_sync(0xffffffffu, corr, 8 * t),
-                  f1 = __shfl_sync(0xffffffffu, corr, 8 * t + 4);
-
-            // ---- values
-            if constexpr (KIND == kQ8) {
-                // the largest value scale of the tile moves the common exponent up
-                __half2 mx = __half2half2(__ushort_as_half(0));
-                uint32_t vsc[4][S::SP / 2];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int key = 2 * t + (x & 1) + (x >> 1) * 8;
-#pragma unroll
-                    for (int w = 0; w < S::SP / 2; ++w) {
-                        uint32_t u = lds32(vsb + key * S::SCB + w * 4);
-                        if (D % 64 != 0 && w == S::SP / 2 - 1)
-                            u &= 0xffffu;  // the odd half is padding
-                        vsc[x][w] = u;
-                        mx = __hmax2(mx, __habs2(*reinterpret_cast<const __half2 *>(&u)));
-                    }
-                }
-                float dm = __half2float(__hmax(__low2half(mx), __high2half(mx)));
-                dm = fmaxf(dm, __shfl_xor_sync(0xffffffffu, dm, 1));
-                dm = fmaxf(dm, __shfl_xor_sync(0xffffffffu, dm, 2));
-                int ve = max(vexp, int(__float_as_uint(dm) >> 23) - 127);
-                if (ve > 15)  // an infinite scale: the others keep theirs
-                    ve = vexp > -126 ? vexp : 15;
-                const float fe = exp2i(max(-126, vexp - ve));
-                f0 *= fe;
-                f1 *= fe;
-                vexp = ve;
-                const float up = exp2i(min(126, 14 - ve));
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    p[x] *= up;
-#pragma unroll
-                for (int blk = 0; blk < D / 32; ++blk) {
-                    uint32_t bh[2], bl[2];
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const float2 s0 = unpack2(vsc[2 * n][blk / 2], __half());
-                        const float2 s1 = unpack2(vsc[2 * n + 1][blk / 2], __half());
-                        const float u0 = p[2 * n] * (blk & 1 ? s0.y : s0.x);
-                        const float u1 = p[2 * n + 1] * (blk & 1 ? s1.y : s1.x);
-                        bh[n] = pack2(u0, u1, H());
-                        const float2 hf = unpack2(bh[n], H());
-                        bl[n] = pack2(u0 - hf.x, u1 - hf.y, H());
-                    }
-                    uint32_t w[4];
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        w[x] = lds32(vb + (2 * t + (x & 1) + (x >> 1) * 8) * S::RS + blk * 32 +
-                                     4 * g) ^ 0x80808080u;
-                    const uint32_t e01 = __byte_perm(w[0], w[1], 0x5140),
-                                   e23 = __byte_perm(w[0], w[1], 0x7362),
-                                   o01 = __byte_perm(w[2], w[3], 0x5140),
-                                   o23 = __byte_perm(w[2], w[3], 0x7362);
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const uint32_t a0 = codes_f16(u ? e23 : e01, 0x4140);
-                        const uint32_t a1 = codes_f16(u ? e23 : e01, 0x4342);
-                        const uint32_t a2 = codes_f16(u ? o23 : o01, 0x4140);
-                        const uint32_t a3 = codes_f16(u ? o23 : o01, 0x4342);
-                        float c[4] = {};
-                        mma<KIND>(c, a0, a1, a2, a3, bl[0], bl[1]);
-                        mma<KIND>(c, a0, a1, a2, a3, bh[0], bh[1]);
-                        float(&o)[4] = O[blk * 2 + u];
-                        o[0] = o[0] * f0 + c[0];
-                        o[1] = o[1] * f1 + c[1];
-                        o[2] = o[2] * f0 + c[2];
-                        o[3] = o[3] * f1 + c[3];
-                    }
-                }
-            } else {
-                uint32_t b[3][2];
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    float u0 = p[2 * n], u1 = p[2 * n + 1];
-#pragma unroll
-                    for (int q = 0; q < (KIND == kBF16 ? 3 : 2); ++q) {
-                        b[q][n] = pack2(u0, u1, H());
-                        const float2 hf = unpack2(b[q][n], H());
-                        u0 -= hf.x;
-                        u1 -= hf.y;
-                    }
-                }
-                const uint32_t vaddr = vb + frag_row;
-#pragma unroll
-                for (int ds = 0; ds < S::KSTEPS; ++ds) {
-                    uint32_t a[4];
-                    ldsm4t(a, S::chunk_at(vaddr, ds));
-                    float c[4] = {};
-                    if constexpr (KIND == kBF16)
-                        mma<KIND>(c, a[0], a[1], a[2], a[3], b[2][0], b[2][1]);
-                    mma<KIND>(c, a[0], a[1], a[2], a[3], b[1][0], b[1][1]);
-                    mma<KIND>(c, a[0], a[1], a[2], a[3], b[0][0], b[0][1]);
-                    O[ds][0] = O[ds][0] * f0 + c[0];
-                    O[ds][1] = O[ds][1] * f1 + c[1];
-                    O[ds][2] = O[ds][2] * f0 + c[2];
-                    O[ds][3] = O[ds][3] * f1 + c[3];
-                }
-            }
-            __syncwarp();
-        }
-        cp_wait<0>();
-        // An infinite value times pieces of a probability (some of them 0 or
-        // negative) gives NaN where the sum is infinite: those columns, if
-        // any, are settled by looking at the values again.
-        bool odd = false;
-#pragma unroll
-        for (int ds = 0; ds < D / 16; ++ds)
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-                odd |= !(fabsf(O[ds][x]) <= FLT_MAX);
-        if (__any_sync(0xffffffffu, odd)) {
-            float inf[D / 16][2] = {};  // sum of the column's infinities and NaNs
-            for (int i = 0; i < nw * kTile; ++i) {
-                uint32_t row;
-                if (!row_of((sp.t0 + ta + warp + i / kTile * kWarps) * kTile + i % kTile, row))
-                    continue;
-#pragma unroll
-                for (int ds = 0; ds < D / 16; ++ds)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const float v = value_at<KIND, D>(C.v, C.vs, row, dim_of<KIND>(ds, g, x));
-                        inf[ds][x] += fabsf(v) <= FLT_MAX ? 0.f : v;
-                    }
-            }
-#pragma unroll
-            for (int ds = 0; ds < D / 16; ++ds)
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    if (!(fabsf(O[ds][x]) <= FLT_MAX) && inf[ds][x >> 1] != 0.f)
-                        O[ds][x] = inf[ds][x >> 1];
-        }
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
-        __syncthreads();  // every warp is done with its ring: it becomes the joining space
-
-        // ---- the warps' results joined
-        auto finish = [&](int h, int d, float4 sum, float M, float tot) {
-            const float inv = tot == 0.f ? 0.f : 1.f / tot;
-            store4_any(A.out, int64_t(seq) * A.ldo + int64_t(head0 + h) * D + d,
-                       make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv), A.dtype);
-            if (A.lse && d == 0)
-                A.lse[int64_t(seq) * A.n_q + head0 + h] =
-                    tot == 0.f ? -INFINITY : (M + log2f(tot) - kBias) * kLn2;
-        };
-        {
-            float undo = 1.f;
-            if constexpr (KIND == kQ8)
-                undo = exp2i(max(-126, vexp - 14));
-            float *o = join + warp * kH * S::OSTRIDE;
-#pragma unroll
-            for (int ds = 0; ds < D / 16; ++ds) {
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    o[(2 * t + (x & 1)) * S::OSTRIDE + dim_of<KIND>(ds, g, x >> 1)] =
-                        O[ds][x] * undo;
-                }
-            }
-            if (t == 0) {
-                join_ml[(warp * kH + g) * 2] = m;
-                join_ml[(warp * kH + g) * 2 + 1] = l;
-            }
-        }
-        __syncthreads();
-        const bool whole = ta == 0 && tb == sp.n;
-        // blocks that share the item
-        const int64_t c0 = whole ? blk : uint64_t(tiles_at) / uint64_t(per);
-        const int64_t c1 = whole ? blk : uint64_t(tiles_at + sp.n - 1) / uint64_t(per);
-        constexpr int PART = kH * (D + 2);  // floats of a partial: [8][D] sums, [8] m, [8] l
-        constexpr int QUADS = D / 4;
-        // A block may be the last of one item and the first of another: a
-        // partial that starts its item goes to the block's second place.
-        float *mine_ws = A.ws + (2 * blk + (ta > 0 ? 0 : 1)) * PART;
-        for (int i = tid; i < nh * QUADS; i += kThreads) {
-            const int h = i / QUADS, d = i % QUADS * 4;
-            float mw[kWarps], M = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                mw[w] = join_ml[(w * kH + h) * 2];
-                M = fmaxf(M, mw[w]);
-            }
-            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-            float tot = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = mw[w] == -INFINITY ? 0.f : ex2(mw[w] - M);
-                add4(sum, f, *reinterpret_cast<const float4 *>(
-                                 join + (w * kH + h) * S::OSTRIDE + d));
-                tot += f * join_ml[(w * kH + h) * 2 + 1];
-            }
-            if (whole) {
-                finish(h, d, sum, M, tot);
-            } else {
-                __stcg(reinterpret_cast<float4 *>(mine_ws + h * D + d), sum);
-                if (d == 0) {
-                    __stcg(mine_ws + kH * D + h, M);
-                    __stcg(mine_ws + kH * D + kH + h, tot);
-                }
-            }
-        }
-        if (!whole) {
-            // ---- the item's last block joins the blocks' partials in block
-            // order; many blocks first join in groups, each group's last block
-            // leaving the group's result in the place of its first
-            const int n = int(c1 - c0) + 1, k = int(blk - c0);
-            const int gs = n <= 16 ? n : (n <= 256 ? 16 : 32);  // blocks of a group
-            float *const start = A.ws + 2 * c0 * PART;
-            auto place = [&](int c) { return start + int64_t(2 * c + (c == 0)) * PART; };
-            // Is this block the last of `of` to count on the ticket?  The
-            // barrier puts every thread's stores before thread 0's release.
-            auto last_of = [&](unsigned *ticket, int of) {
-                __syncthreads();
-                if (tid == 0) {
-                    unsigned before;
-                    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;"
-                                 : "=r"(before)
-                                 : "l"(ticket)
-                                 : "memory");
-                    last_block = before == unsigned(of - 1);
-                    if (last_block)
-                        *ticket = 0;
-                }
-                __syncthreads();
-                return last_block;
-            };
-            // Sum of `count` partials `step` blocks apart, from block `from`
-            // of the item on; sixteen are under way at once.
-            auto join_parts = [&](int from, int step, int count, int h, int d, float4 &sum,
-                                  float &M, float &tot) {
-                sum = make_float4(0.f, 0.f, 0.f, 0.f);
-                M = -INFINITY;
-                tot = 0.f;
-                for (int c = 0; c < count; c += 16) {
-                    float4 o[16];
-                    float pm[16], pl[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float *w = place(from + min(c + j, count - 1) * step);
-                        o[j] = __ldcg(reinterpret_cast<const float4 *>(w + h * D + d));
-                        pm[j] = c + j < count ? __ldcg(w + kH * D + h) : -INFINITY;
-                        pl[j] = __ldcg(w + kH * D + kH + h);
-                    }
-                    float mn = M;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        mn = fmaxf(mn, pm[j]);
-                    const float f = M == -INFINITY ? 0.f : ex2(M - mn);
-                    sum = make_float4(sum.x * f, sum.y * f, sum.z * f, sum.w * f);
-                    tot *= f;
-                    M = mn;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        if (c + j >= count)
-                            continue;
-                        const float fj = pm[j] == -INFINITY ? 0.f : ex2(pm[j] - mn);
-                        add4(sum, fj, o[j]);
-                        tot += fj * pl[j];
-                    }
-                }
-            };
-            const int grp = k / gs, first = grp * gs, size = min(gs, n - first);
-            bool mine_to_join = last_of(
-                A.tickets + (grp ? A.max_blocks + c0 + first : c0), size);
-            if (mine_to_join && gs < n) {
-                constexpr int PER = (kH * QUADS + kThreads - 1) / kThreads;
-                float4 sum[PER];
-                float M[PER], tot[PER];
-#pragma unroll
-                for (int u = 0; u < PER; ++u) {
-                    const int i = tid + u * kThreads;
-                    if (i < nh * QUADS)
-                        join_parts(first, 1, size, i / QUADS, i % QUADS * 4, sum[u], M[u], tot[u]);
-                }
-                __syncthreads();  // everything is read before the first place is overwritten
-                float *w = place(first);
-#pragma unroll
-                for (int u = 0; u < PER; ++u) {
-                    const int i = tid + u * kThreads, h = i / QUADS, d = i % QUADS * 4;
-                    if (i >= nh * QUADS)
-                        continue;
-                    __stcg(reinterpret_cast<float4 *>(w + h * D + d), sum[u]);
-                    if (d == 0) {
-                        __stcg(w + kH * D + h, M[u]);
-                        __stcg(w + kH * D + kH + h, tot[u]);
-                    }
-                }
-                mine_to_join = last_of(A.tickets + 2 * A.max_blocks + c0, (n + gs - 1) / gs);
-            }
-            if (mine_to_join) {
-                for (int i = tid; i < nh * QUADS; i += kThreads) {
-                    const int h = i / QUADS, d = i % QUADS * 4;
-                    float4 sum;
-                    float M, tot;
-                    if (gs < n)
-                        join_parts(0, gs, (n + gs - 1) / gs, h, d, sum, M, tot);
-                    else
-                        join_parts(0, 1, n, h, d, sum, M, tot);
-                    finish(h, d, sum, M, tot);
-                }
-            }
-        }
-        __syncthreads();  // the joining space becomes the ring again
-    }
-}
-
-template <Kind KIND, int D>
-cudaError_t launch_dim(AttnParams &p, int sm_count, cudaStream_t s)
-{
-    using Sh = Shape<KIND, D>;
-    const auto kern = attn_kernel<KIND, D>;
-    const void *f = reinterpret_cast<const void *>(kern);
-    cudaError_t e = func_smem(f, Sh::SMEM, true);
-    if (e != cudaSuccess)
-        return e;
-    int occ = 0;
-    e = func_occupancy(f, kThreads, Sh::SMEM, &occ);
-    if (e != cudaSuccess)
-        return e;
-    if (occ < 1)
-        return cudaErrorInvalidConfiguration;
-    p.min_units = kMinUnits;
-    const int64_t longest = std::min<int64_t>(p.a.ld_table * p.a.c.page_size, 0x7fffffe0);
-    const int64_t units =
-        int64_t(p.a.n_seqs) * p.items * ((longest + kTile - 1) / kTile + 1 + kItemCost);
-    int64_t grid = std::min<int64_t>(int64_t(occ) * sm_count, p.a.max_blocks);
-    grid = std::max<int64_t>(1, std::min<int64_t>(grid, units / p.min_units + 1));
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(grid));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Sh::SMEM;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = pdl_enabled() ? 1 : 0;
-    return counted(cudaLaunchKernelEx(&cfg, kern, p));
-}
-
-template <Kind KIND>
-cudaError_t launch_kind(AttnParams &p, int sm_count, cudaStream_t s)
-{
-    switch (p.a.c.D) {
-    case 64: return launch_dim<KIND, 64>(p, sm_count, s);
-    case 96: return launch_dim<KIND, 96>(p, sm_count, s);
-    case 128: return launch_dim<KIND, 128>(p, sm_count, s);
-    case 192: return launch_dim<KIND, 192>(p, sm_count, s);
-    case 256: return launch_dim<KIND, 256>(p, sm_count, s);
-    }
-    return cudaErrorInvalidValue;
-}
-
-} // namespace
 
 bool attn_takes_head_dim(int D)
 {
     return D == 64 || D == 96 || D == 128 || D == 192 || D == 256;
 }
 
-size_t attn_partial_floats(int D) { return size_t(kH) * size_t(D + 2); }
+size_t attn_partial_floats(int D) { return size_t(kAttnHeads) * size_t(D + 2); }
 
 cudaError_t launch_attn_decode(const AttnArgs &a, int sm_count, cudaStream_t s)
 {
@@ -1037,12 +18,10 @@ cudaError_t launch_attn_decode(const AttnArgs &a, int sm_count, cudaStream_t s)
     memset(static_cast<void *>(&p), 0, sizeof(p));
     p.a = a;
     p.group = a.n_q / a.c.n_heads;
-    p.head_tiles = (p.group + kH - 1) / kH;
-    p.items = a.c.n_heads * p.head_tiles;
     switch (a.type) {
-    case QMM_F16: return launch_kind<kF16>(p, sm_count, s);
-    case QMM_BF16: return launch_kind<kBF16>(p, sm_count, s);
-    default: return launch_kind<kQ8>(p, sm_count, s);
+    case QMM_F16: return launch_attn_f16(p, sm_count, s);
+    case QMM_BF16: return launch_attn_bf16(p, sm_count, s);
+    default: return launch_attn_q8(p, sm_count, s);
     }
 }
 

@@ -446,7 +446,7 @@ struct KvReadArgs {
 cudaError_t launch_kv_read(const KvReadArgs &a, int sm_count, cudaStream_t s);
 
 // Attention of one new token per sequence (attn_decode.cu).
-constexpr int kAttnHeads = 8;      // query heads of one kv head that a block takes together
+constexpr int kAttnHeads = 8;  // query heads of one kv head that a block takes at most
 struct AttnArgs {
     KvView c;
     int type, dtype;
@@ -465,9 +465,20 @@ struct AttnArgs {
     unsigned *tickets, *status;
     int max_blocks;
 };
+struct AttnParams {
+    AttnArgs a;
+    int group;          // query heads per kv head
+    int head_tiles;     // ceil(group / heads of a tile)
+    int items;          // kv heads * head tiles
+    int min_units;      // units (16-key tiles, and kItemCost an item) a block takes at least
+};
 bool attn_takes_head_dim(int D);
 size_t attn_partial_floats(int D);  // floats of one partial result
 cudaError_t launch_attn_decode(const AttnArgs &a, int sm_count, cudaStream_t s);
+// attn_f16.cu, attn_bf16.cu, attn_q8.cu
+cudaError_t launch_attn_f16(AttnParams &p, int sm_count, cudaStream_t s);
+cudaError_t launch_attn_bf16(AttnParams &p, int sm_count, cudaStream_t s);
+cudaError_t launch_attn_q8(AttnParams &p, int sm_count, cudaStream_t s);
 
 // --------------------------------------------------------------- logits
 struct LogitsArgs {
