@@ -107,6 +107,24 @@ struct Shape {
     static constexpr int RING = W * STAGES * STAGE;
     static constexpr int SMEM = QFRAG + (RING > JOIN ? RING : JOIN);
     static_assert(STAGES >= 2, "ring");
+    // Where the 16-byte chunk it * 32 + lane of a tile's contiguous rows goes;
+    // copy_base is the lane's part of it where rows are powers of two.
+    static constexpr bool POW2 = 32 % CHUNKS == 0;
+    static __device__ __forceinline__ uint32_t copy_base(int lane)
+    {
+        const int r = lane / CHUNKS, ch = lane % CHUNKS;
+        return r * RS + (SWZ ? ch ^ r : ch) * 16;
+    }
+    static __device__ __forceinline__ uint32_t copy_at(uint32_t base, int it, int lane)
+    {
+        if constexpr (POW2) {
+            constexpr int R = 32 / CHUNKS;  // rows of an instruction
+            return (SWZ ? base ^ ((it * R & 7) * 16) : base) + it * R * RS;
+        } else {
+            const int idx = it * 32 + lane, r = idx / CHUNKS, ch = idx % CHUNKS;
+            return r * RS + (SWZ ? ch ^ (r & 7) : ch) * 16;
+        }
+    }
     // Address of 16-value column ks of a row, from that of column 0.
     static __device__ __forceinline__ uint32_t chunk_at(uint32_t row, int ks)
     {
@@ -125,6 +143,10 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void *src, unsigned byt
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                  : "memory");
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp4(uint32_t dst, const void *src, unsigned bytes)
 {
@@ -157,6 +179,27 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr)
     uint32_t v;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
+}
+// N words from a 4-byte boundary (one load where N is 1, 2 or 4 and the
+// address a multiple of their size).
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t (&v)[N], uint32_t addr)
+{
+    if constexpr (N == 2) {
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
+                     : "=r"(v[0]), "=r"(v[1])
+                     : "r"(addr)
+                     : "memory");
+    } else if constexpr (N == 4) {
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                     : "r"(addr)
+                     : "memory");
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] = lds32(addr + 4 * i);
+    }
 }
 __device__ __forceinline__ uint2 lds64(uint32_t addr)
 {
@@ -191,6 +234,12 @@ __device__ __forceinline__ float2 unpack2(uint32_t u, __half)
 __device__ __forceinline__ float2 unpack2(uint32_t u, __nv_bfloat16)
 {
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+
+// Two of four bytes u as f16 subnormals u * 2^-24 (exact operands).
+__device__ __forceinline__ uint32_t bytes_f16(uint32_t u, unsigned sel)
+{
+    return __byte_perm(u, 0u, sel);
 }
 
 // Four int8 codes, as bytes code + 128, to two pairs of f16: 1024 + byte by
@@ -282,6 +331,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
     __shared__ unsigned valid_ring[kWarps][STAGES];
     __shared__ int qexp[NH];
     __shared__ bool qfinite[NH];
+    __shared__ float q_off[NH][D / 32];
     __shared__ bool last_block;
 
     const AttnArgs &A = P.a;
@@ -291,88 +341,136 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
     pdl_wait();
     pdl_launch_dependents();
 
-    // ---- the plan: prefix sums of the sequences' tiles
-    for (int b = tid; b < min(A.n_seqs, kLens); b += kThreads)
-        lens[b] = __ldg(A.lens + b);
-    __syncthreads();
+    // ---- the plan: prefix sums of the sequences' units
     auto units_of = [&](int n) { return n ? int64_t(n + kItemCost) * P.items : int64_t(0); };
     auto len_of = [&](int b) { return b < kLens ? lens[b] : __ldg(A.lens + b); };
-    const int per_thread = (A.n_seqs + kThreads - 1) / kThreads;
-    const int sb0 = min(A.n_seqs, tid * per_thread), sb1 = min(A.n_seqs, sb0 + per_thread);
-    int64_t mine = 0;
-    int most = 0;
-    for (int b = sb0; b < sb1; ++b) {
-        const int len = len_of(b);
-        const Span sp = span_of(A, len);
-        mine += units_of(sp.n);
-        most = max(most, sp.n);
-        if (blockIdx.x == 0 && (len < 0 || len > sp.hi))
-            atomicOr(A.status, kStatusBadLengthBit);
-    }
-    // sequences without keys are no one's item: their outputs are zero
-    for (int b = blockIdx.x; b < A.n_seqs; b += gridDim.x) {
-        if (span_of(A, len_of(b)).n > 0)
-            continue;
-        for (int i = tid; i < A.n_q * D / 4; i += kThreads)
-            store4_any(A.out, b * A.ldo + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f), A.dtype);
-        if (A.lse)
-            for (int i = tid; i < A.n_q; i += kThreads)
-                A.lse[int64_t(b) * A.n_q + i] = -INFINITY;
-    }
-    int64_t upto = mine;  // units of the sequences up to this thread's
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-        upto += lane >= o ? v : 0;
-    }
-    most = __reduce_max_sync(0xffffffffu, most);
-    if (lane == 31) {
-        warp_units[warp] = upto;
-        warp_longest[warp] = most;
-    }
-    __syncthreads();
-    int64_t total = 0;
-    int longest = 0;  // tiles of the longest item
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        upto += w < warp ? warp_units[w] : 0;
-        total += warp_units[w];
-        longest = max(longest, warp_longest[w]);
-    }
-    if (total == 0)
-        return;
+    // Sequences without keys are no one's item: their outputs are zero.
+    auto fill_empty = [&]() {
+        for (int b = blockIdx.x; b < A.n_seqs; b += gridDim.x) {
+            if (span_of(A, __ldg(A.lens + b)).n > 0)
+                continue;
+            for (int i = tid; i < A.n_q * D / 4; i += kThreads)
+                store4_any(A.out, b * A.ldo + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f), A.dtype);
+            if (A.lse)
+                for (int i = tid; i < A.n_q; i += kThreads)
+                    A.lse[int64_t(b) * A.n_q + i] = -INFINITY;
+        }
+    };
     // Block c takes units [c * per, (c + 1) * per): unit x is block x / per's.
     // Equal shares for all resident blocks, but no smaller ones than pay for
     // a join; those small ones divide the longest item evenly.
-    const unsigned whole_item = unsigned(longest + kItemCost);
-    const unsigned parts = max(1u, whole_item / unsigned(P.min_units));
-    const int64_t per = max(int64_t((whole_item + parts - 1) / parts),
-                            int64_t((uint64_t(total) + gridDim.x - 1) / gridDim.x));
-    const int64_t blk = blockIdx.x, r0 = per * blk, r1 = min(total, r0 + per);
-    if (r0 >= total)
-        return;
-    if (r0 < upto && r0 >= upto - mine) {
-        int64_t at = upto - mine;
-        for (int b = sb0; b < sb1; ++b) {
-            const int64_t n = units_of(span_of(A, len_of(b)).n);
-            if (r0 < at + n) {
-                found_seq = b;
-                found_at = at;
-                break;
-            }
-            at += n;
+    auto share = [&](int64_t total, int longest) {
+        const unsigned item = unsigned(longest + kItemCost);
+        const unsigned parts = max(1u, item / unsigned(P.min_units));
+        const int64_t even = total <= 0xffffffffll
+                                 ? int64_t((unsigned(total) - 1) / gridDim.x + 1)
+                                 : (total - 1) / int64_t(gridDim.x) + 1;
+        return max(int64_t((item + parts - 1) / parts), even);
+    };
+    int64_t total = 0, per, r0, seq_at;
+    int seq, seq_len;
+    if (A.n_seqs <= 32) {
+        // every warp by itself, a sequence a lane
+        const int len = lane < A.n_seqs ? __ldg(A.lens + lane) : 0;
+        const Span sp = span_of(A, len);
+        if (blockIdx.x == 0 && warp == 0 && (len < 0 || len > sp.hi))
+            atomicOr(A.status, kStatusBadLengthBit);
+        if (warp == 0)
+            lens[lane] = len;  // (read after later barriers)
+        const int64_t mine = units_of(sp.n);
+        int64_t upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+            upto += lane >= o ? v : 0;
         }
+        total = __shfl_sync(0xffffffffu, upto, 31);
+        if (total == 0) {
+            fill_empty();
+            return;
+        }
+        per = share(total, __reduce_max_sync(0xffffffffu, sp.n));
+        r0 = per * blockIdx.x;
+        const unsigned past = __ballot_sync(0xffffffffu, upto > r0);
+        if (!past) {
+            fill_empty();
+            return;
+        }
+        seq = __ffs(past) - 1;
+        seq_at = __shfl_sync(0xffffffffu, upto - mine, seq);
+        seq_len = __shfl_sync(0xffffffffu, len, seq);
+    } else {
+        for (int b = tid; b < min(A.n_seqs, kLens); b += kThreads)
+            lens[b] = __ldg(A.lens + b);
+        __syncthreads();
+        const int per_thread = (A.n_seqs + kThreads - 1) / kThreads;
+        const int sb0 = min(A.n_seqs, tid * per_thread), sb1 = min(A.n_seqs, sb0 + per_thread);
+        int64_t mine = 0;
+        int most = 0;
+        for (int b = sb0; b < sb1; ++b) {
+            const int len = len_of(b);
+            const Span sp = span_of(A, len);
+            mine += units_of(sp.n);
+            most = max(most, sp.n);
+            if (blockIdx.x == 0 && (len < 0 || len > sp.hi))
+                atomicOr(A.status, kStatusBadLengthBit);
+        }
+        int64_t upto = mine;  // units of the sequences up to this thread's
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+            upto += lane >= o ? v : 0;
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 31) {
+            warp_units[warp] = upto;
+            warp_longest[warp] = most;
+        }
+        __syncthreads();
+        int longest = 0;  // tiles of the longest item
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            upto += w < warp ? warp_units[w] : 0;
+            total += warp_units[w];
+            longest = max(longest, warp_longest[w]);
+        }
+        if (total == 0) {
+            fill_empty();
+            return;
+        }
+        per = share(total, longest);
+        r0 = per * blockIdx.x;
+        if (r0 >= total) {
+            fill_empty();
+            return;
+        }
+        if (r0 < upto && r0 >= upto - mine) {
+            int64_t at = upto - mine;
+            for (int b = sb0; b < sb1; ++b) {
+                const int64_t n = units_of(span_of(A, len_of(b)).n);
+                if (r0 < at + n) {
+                    found_seq = b;
+                    found_at = at;
+                    break;
+                }
+                at += n;
+            }
+        }
+        __syncthreads();
+        seq = found_seq;
+        seq_at = found_at;
+        seq_len = len_of(seq);
     }
-    __syncthreads();
-    int seq = found_seq;
-    int64_t seq_at = found_at;
-    Span sp = span_of(A, len_of(seq));
+    const int64_t blk = blockIdx.x, r1 = min(total, r0 + per);
+    Span sp = span_of(A, seq_len);
 
     const uint32_t smem_base = smem_u32(smem);
     // this lane's row and half-chunk of an ldmatrix over 16 keys x 16 values
     const uint32_t frag_row =
         ((lane >> 4) * 8 + (lane & 7)) * S::RS +
         (S::SWZ ? ((lane >> 3) & 1) ^ (lane & 7) : (lane >> 3) & 1) * 16;
+    const uint32_t copy_row = S::copy_base(lane);
+    const bool whole_tiles = C.page.d % kTile == 0;  // a tile lies in one page
     const uint32_t ring = smem_base + S::QFRAG + warp * STAGES * S::STAGE;
     float *join = reinterpret_cast<float *>(smem + S::QFRAG);
     float *join_ml = join + kWarps * NH * S::OSTRIDE;
@@ -417,7 +515,33 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
             return unsigned(id) < C.n_pages;
         };
         auto issue = [&](int i, int id) {
-            if (i < nw) {
+            const int first = (sp.t0 + ta + warp + i * kWarps) * kTile;
+            if (i < nw && whole_tiles && first >= sp.lo && first + kTile <= sp.hi &&
+                unsigned(id) < C.n_pages) {
+                // sixteen keys of one page: contiguous rows
+                const int st = i % STAGES;
+                if (lane == 0)
+                    valid_ring[warp][st] = 0xffffu;
+                const uint32_t kdst = ring + st * S::STAGE, vdst = kdst + kTile * S::RS;
+                const uint32_t row =
+                    (uint32_t(id) * unsigned(C.n_heads) + unsigned(kvh)) * C.page.d +
+                    unsigned(first) - fast_div(C.page, unsigned(first)) * C.page.d;
+                const uint64_t o = uint64_t(row) * S::ROWB + lane * 16;
+                const uint8_t *ksrc = C.k + o, *vsrc = C.v + o;
+#pragma unroll
+                for (int it = 0; it < kTile * S::CHUNKS / 32; ++it) {
+                    const uint32_t at = S::copy_at(copy_row, it, lane);
+                    cp16(kdst + at, ksrc + it * 512);
+                    cp16(vdst + at, vsrc + it * 512);
+                }
+                if constexpr (KIND == kQ8) {  // SCB chunks of scales, lanes 0.. keys', 16.. values'
+                    const uint8_t *ssrc = static_cast<const uint8_t *>(lane < 16 ? C.ks : C.vs);
+                    if ((lane & 15) < S::SCB)
+                        cp16(kdst + 2 * kTile * S::RS + (lane >> 4) * kTile * S::SCB +
+                                 (lane & 15) * 16,
+                             ssrc + uint64_t(row) * S::SCB + (lane & 15) * 16);
+                }
+            } else if (i < nw) {
                 const int j = key_of(i);
                 const bool ok = unsigned(id) < C.n_pages;
                 if (!ok && j >= sp.lo && j < sp.hi)
@@ -515,7 +639,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
                 // the largest component to [2^13, 2^14)
                 e = max(-126, min(126, 13 - (int(__float_as_uint(mx) >> 23) - 127)));
             }
-            if (h < NH) {
+            if (tid < 16 * NH) {  // (whole warps)
                 if (lt == 0) {
                     qexp[h] = e;
                     qfinite[h] = sum == 0.f;
@@ -523,6 +647,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
                 uint16_t *frag = reinterpret_cast<uint16_t *>(smem);
                 uint16_t *frag3 = reinterpret_cast<uint16_t *>(smem + S::KSTEPS * 512);
                 const float f = exp2i(e);
+                float off[D / 32] = {};
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
                     const int d = i * 16 + lt;
@@ -546,6 +671,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
                     const H p0 = H(x);
                     const float r1 = x - float(p0);
                     const H p1 = H(r1);
+                    off[i / 2] += float(p0) + float(p1);
                     put(h, p0);
                     put(h + NH, p1);
                     if constexpr (NH == 4) {
@@ -557,12 +683,29 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
                             *reinterpret_cast<const uint16_t *>(&p2);
                     }
                 }
+                if constexpr (KIND == kQ8) {  // -128 * 2^-24 times each block's sum of q
+#pragma unroll
+                    for (int blk = 0; blk < D / 32; ++blk) {
+#pragma unroll
+                        for (int o = 1; o < 16; o <<= 1)
+                            off[blk] += __shfl_xor_sync(0xffffffffu, off[blk], o);
+                        if (lt == 0)
+                            q_off[h][blk] = off[blk] * -0x1p-17f;
+                    }
+                }
             }
         }
         __syncthreads();
 
         const int hd = g & (NH - 1);  // the head whose scores this lane holds
-        const float qscale = A.scale * exp2i(-qexp[hd]);
+        const float qscale =
+            A.scale * exp2i(-qexp[hd]) * (KIND == kQ8 ? 0x1p24f : 1.f);
+        float qoff[D / 32];
+        if constexpr (KIND == kQ8) {
+#pragma unroll
+            for (int blk = 0; blk < D / 32; ++blk)
+                qoff[blk] = g < NH ? q_off[hd][blk] : 0.f;
+        }
         const float cap_inv = A.softcap > 0.f ? 1.f / A.softcap : 0.f;
         const float slope =
             A.alibi && hd < nh ? __ldg(A.alibi + head0 + hd) * kLog2e : 0.f;
@@ -585,34 +728,43 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
             float s[4];
             if constexpr (KIND == kQ8) {
                 s[0] = s[1] = s[2] = s[3] = 0.f;
+                uint32_t ksc[4][S::SP / 2];
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    lds_words(ksc[x], ksb + (2 * t + (x & 1) + (x >> 1) * 8) * S::SCB);
 #pragma unroll
                 for (int blk = 0; blk < D / 32; ++blk) {
-                    float c0[4] = {}, c1[4] = {};
-                    const uint4 a0 = *reinterpret_cast<const uint4 *>(
-                        smem + ((2 * blk) * 32 + lane) * 16);
-                    const uint4 a1 = *reinterpret_cast<const uint4 *>(
-                        smem + ((2 * blk + 1) * 32 + lane) * 16);
-                    uint2 w = lds64(kb + g * S::RS + blk * 32 + t * 8);
-                    w.x ^= 0x80808080u;
-                    w.y ^= 0x80808080u;
-                    mma<KIND>(c0, a0.x, a0.y, a0.z, a0.w, codes_f16(w.x, 0x4140),
-                              codes_f16(w.x, 0x4342));
-                    mma<KIND>(c0, a1.x, a1.y, a1.z, a1.w, codes_f16(w.y, 0x4140),
-                              codes_f16(w.y, 0x4342));
-                    w = lds64(kb + (g + 8) * S::RS + blk * 32 + t * 8);
-                    w.x ^= 0x80808080u;
-                    w.y ^= 0x80808080u;
-                    mma<KIND>(c1, a0.x, a0.y, a0.z, a0.w, codes_f16(w.x, 0x4140),
-                              codes_f16(w.x, 0x4342));
-                    mma<KIND>(c1, a1.x, a1.y, a1.z, a1.w, codes_f16(w.y, 0x4140),
-                              codes_f16(w.y, 0x4342));
+                    // codes + 128 as subnormals; the 128s' part of the sum, which
+                    // is q's, is where it starts from
+                    uint4 a[2];
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int key = 2 * t + (x & 1) + (x >> 1) * 8;
-                        const __half *sc = reinterpret_cast<const __half *>(
-                            smem + (ksb - smem_base) + key * S::SCB);
-                        const float *cc = x < 2 ? c0 : c1;
-                        s[x] += (cc[x & 1] + cc[2 + (x & 1)]) * __half2float(sc[blk]);
+                    for (int u = 0; u < 2; ++u) {
+                        const uint8_t *fr = smem + ((2 * blk + u) * 32 + lane) * 16;
+                        if constexpr (NH == 8) {
+                            a[u] = *reinterpret_cast<const uint4 *>(fr);
+                        } else {  // rows 8-15 are empty
+                            a[u].x = *reinterpret_cast<const uint32_t *>(fr);
+                            a[u].y = 0u;
+                            a[u].z = *reinterpret_cast<const uint32_t *>(fr + 8);
+                            a[u].w = 0u;
+                        }
+                    }
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        float c[4] = {qoff[blk], qoff[blk], 0.f, 0.f};
+                        uint2 w = lds64(kb + (g + n * 8) * S::RS + blk * 32 + t * 8);
+                        w.x ^= 0x80808080u;
+                        w.y ^= 0x80808080u;
+                        mma<KIND>(c, a[0].x, a[0].y, a[0].z, a[0].w, bytes_f16(w.x, 0x4140),
+                                  bytes_f16(w.x, 0x4342));
+                        mma<KIND>(c, a[1].x, a[1].y, a[1].z, a[1].w, bytes_f16(w.y, 0x4140),
+                                  bytes_f16(w.y, 0x4342));
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const float2 sc = unpack2(ksc[2 * n + y][blk / 2], __half());
+                            s[2 * n + y] += (NH == 8 ? c[y] + c[2 + y] : c[y]) *
+                                            (blk & 1 ? sc.y : sc.x);
+                        }
                     }
                 }
             } else {
@@ -666,20 +818,31 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
                     for (int d = 0; d < D; ++d)
                         dot += load_any(A.q, q0 + d, A.dtype) *
                                value_at<KIND, D>(C.k, C.ks, row, d);
-                    s[x] = dot * exp2i(qexp[hd]);
+                    s[x] = dot * exp2i(qexp[hd]) * (KIND == kQ8 ? 0x1p-24f : 1.f);
                 }
             }
-            float tmax = -INFINITY;
+            // scores in base 2
+            if (A.softcap > 0.f) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int key = 2 * t + (x & 1) + (x >> 1) * 8;
-                float v = s[x] * qscale;
-                if (A.softcap > 0.f)
-                    v = A.softcap * tanhf(v * cap_inv);
-                v = v * kLog2e + slope * float(key0 + key - (sp.hi - 1));
-                s[x] = (valid >> key) & 1u ? v : -INFINITY;
-                tmax = fmaxf(tmax, s[x]);
+                for (int x = 0; x < 4; ++x)
+                    s[x] = A.softcap * kLog2e * tanhf(s[x] * qscale * cap_inv);
+            } else {
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    s[x] *= qscale * kLog2e;
             }
+            if (A.alibi) {
+                const float back = float(key0 + 2 * t - (sp.hi - 1));
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    s[x] += slope * (back + float((x & 1) + (x >> 1) * 8));
+            }
+            if (valid != 0xffffu) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    s[x] = (valid >> (2 * t + (x & 1) + (x >> 1) * 8)) & 1u ? s[x] : -INFINITY;
+            }
+            float tmax = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
             tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 1));
             tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 2));
             const float mn = fmaxf(m, tmax);
@@ -704,15 +867,12 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
                 uint32_t vsc[4][S::SP / 2];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const int key = 2 * t + (x & 1) + (x >> 1) * 8;
+                    lds_words(vsc[x], vsb + (2 * t + (x & 1) + (x >> 1) * 8) * S::SCB);
+                    if (D % 64 != 0)
+                        vsc[x][S::SP / 2 - 1] &= 0xffffu;  // the odd half is padding
 #pragma unroll
-                    for (int w = 0; w < S::SP / 2; ++w) {
-                        uint32_t u = lds32(vsb + key * S::SCB + w * 4);
-                        if (D % 64 != 0 && w == S::SP / 2 - 1)
-                            u &= 0xffffu;  // the odd half is padding
-                        vsc[x][w] = u;
-                        mx = __hmax2(mx, __habs2(*reinterpret_cast<const __half2 *>(&u)));
-                    }
+                    for (int w = 0; w < S::SP / 2; ++w)
+                        mx = __hmax2(mx, __habs2(*reinterpret_cast<const __half2 *>(&vsc[x][w])));
                 }
                 float dm = __half2float(__hmax(__low2half(mx), __high2half(mx)));
                 dm = fmaxf(dm, __shfl_xor_sync(0xffffffffu, dm, 1));
@@ -1011,6 +1171,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
         }
         __syncthreads();  // the joining space becomes the ring again
     }
+    fill_empty();
 }
 
 template <Kind KIND, int D, int NH>
