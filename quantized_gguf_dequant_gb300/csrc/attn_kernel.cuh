@@ -227,15 +227,6 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
 template <Kind KIND>
 using Half = typename std::conditional<KIND == kBF16, __nv_bfloat16, __half>::type;
 
-__device__ __forceinline__ float2 unpack2(uint32_t u, __half)
-{
-    return __half22float2(*reinterpret_cast<const __half2 *>(&u));
-}
-__device__ __forceinline__ float2 unpack2(uint32_t u, __nv_bfloat16)
-{
-    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-}
-
 // Two of four bytes u as f16 subnormals u * 2^-24 (exact operands).
 __device__ __forceinline__ uint32_t bytes_f16(uint32_t u, unsigned sel)
 {

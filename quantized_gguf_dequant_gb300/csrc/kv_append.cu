@@ -11,12 +11,13 @@
 // Bytes bound it: q, k and v are read once, q_out and the cache rows written
 // once.  A block takes one token (or, when there are few tokens, one part of
 // its heads, so that a decode step spreads over the SMs): the token's cosines
-// and sines are computed once into shared memory and serve all its heads.  A
-// warp owns whole rows of D values, four to a lane; it holds a row and the
-// row's partners in registers before it stores anything, so q_out may be q.
-// A Q8_0 block of 32 values is eight lanes.
+// and sines are computed once into shared memory and serve all its heads,
+// while the first rows' loads are already under way.  A lane holds its part of
+// a row in registers before it stores any of it, so q_out may be q.  A Q8_0
+// block of 32 values is eight lanes of fp32 or four of 16-bit values.
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 #include "kv_cache.cuh"
 #include "qmm_device.cuh"
@@ -31,40 +32,82 @@ constexpr int kWarps = kThreads / 32;
 
 enum Kind { kF16, kBF16, kQ8 };
 
-// Four rounded values of a Q8_0 block held by eight lanes (scale = amax/127,
-// code = rint(x / scale), the scale kept in fp16).
-__device__ __forceinline__ uint32_t quantize4(float4 x, float &d)
-{
-    float amax = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
-    // a NaN must reach the stored scale: fmaxf would drop it
-    const bool nan = x.x != x.x || x.y != x.y || x.z != x.z || x.w != x.w;
+// 16 bytes of values.
+template <typename IO>
+struct Chunk {
+    static constexpr int N = 16 / sizeof(IO);
+    uint4 raw;
+    __device__ __forceinline__ void load(const IO *p) { raw = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void values(float (&v)[N]) const
+    {
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1)
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(IO) == 4) {
+                v[i] = __uint_as_float(w[i]);
+            } else {
+                const float2 f = unpack2(w[i], IO());
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+            }
+        }
+    }
+};
+
+// N (4 or 8) values to consecutive places of a type.
+template <int N, typename T>
+__device__ __forceinline__ void store_values(T *p, const float (&v)[N])
+{
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    } else if constexpr (N == 8) {
+        *reinterpret_cast<uint4 *>(p) =
+            make_uint4(pack2(v[0], v[1], T()), pack2(v[2], v[3], T()), pack2(v[4], v[5], T()),
+                       pack2(v[6], v[7], T()));
+    } else {
+        *reinterpret_cast<uint2 *>(p) =
+            make_uint2(pack2(v[0], v[1], T()), pack2(v[2], v[3], T()));
+    }
+}
+
+// A Q8_0 block of 32 values, N to a lane: scale = amax/127, code =
+// rint(x / scale) in fp32.  Every lane of the warp calls it.
+template <int N>
+__device__ __forceinline__ void quantize(const float (&x)[N], uint32_t (&codes)[N / 4], float &d)
+{
+    constexpr int LANES = 32 / N;
+    float amax = 0.f, nan = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        amax = fmaxf(amax, fabsf(x[i]));
+        nan += x[i] * 0.f;
+    }
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1)
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const unsigned lanes = __ballot_sync(0xffffffffu, nan);
-    if ((lanes >> (threadIdx.x & 24)) & 0xffu)
+    // a NaN must reach the stored scale: fmaxf drops it
+    const unsigned bad = __ballot_sync(0xffffffffu, !(nan == 0.f) && !(amax == INFINITY));
+    if ((bad >> (threadIdx.x & (32 - LANES))) & ((1u << LANES) - 1))
         amax = __int_as_float(0x7fc00000);
     d = __fdiv_rn(amax, 127.f);
     const float inv = d > 0.f ? __fdiv_rn(1.f, d) : 0.f;
-    auto code = [&](float v) {
-        return uint32_t(__float2int_rn(__fmul_rn(v, inv))) & 0xffu;
-    };
-    return code(x.x) | (code(x.y) << 8) | (code(x.z) << 16) | (code(x.w) << 24);
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        uint32_t w = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w |= (uint32_t(__float2int_rn(__fmul_rn(x[i + j], inv))) & 0xffu) << (8 * j);
+        codes[i / 4] = w;
+    }
 }
 
-template <Kind KIND, typename IO, int D>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs P)
+// The token's cosines and sines, and where its rows go: slot's row of head 0,
+// or -1 for a token that is not stored.
+__device__ __forceinline__ void turns_of(const AppendArgs &P, int64_t tok, float2 *turn)
 {
-    constexpr int LPR = D / 4 < 32 ? D / 4 : 32;         // lanes per row
-    constexpr int RPW = D <= 64 ? 32 / LPR : 1;          // rows per warp and pass
-    constexpr int PASSES = (D + 127) / 128;
-    constexpr int SP = kv_scales_per_row(D);
-    __shared__ float2 turn[128];  // (cos, sin) of each pair
-    pdl_wait();
-    pdl_launch_dependents();
-    const int64_t tok = blockIdx.x;
-    const int half = P.n_rot >> 1;
-    for (int i = threadIdx.x; i < half; i += kThreads) {
+    for (int i = threadIdx.x; i < P.n_rot >> 1; i += kThreads) {
         int ax = 0;
         while (i >= P.axis_end[ax])
             ++ax;
@@ -74,140 +117,297 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
         sincosf(angle, &sn, &cn);
         turn[i] = make_float2(cn, sn);
     }
-    __syncthreads();
-    const int64_t slot = __ldg(P.slots + tok);
+}
+__device__ __forceinline__ int64_t row_of_slot(const AppendArgs &P, int64_t slot)
+{
     const KvView &c = P.c;
     const bool stored = slot >= 0 && slot < int64_t(c.n_pages) * c.page_size;
     if (slot >= 0 && !stored && threadIdx.x == 0 && blockIdx.y == 0)
         atomicOr(P.status, kStatusBadSlotBit);
-    int64_t row0 = 0;
-    if (stored) {
-        const int64_t page = slot / c.page_size;
-        row0 = page * c.n_heads * c.page_size + (slot - page * c.page_size);
+    if (!stored)
+        return -1;
+    const uint32_t page = uint32_t(uint64_t(slot) / uint32_t(c.page_size));
+    return int64_t(page) * c.n_heads * c.page_size +
+           (slot - int64_t(page) * c.page_size);
+}
+
+// N values of a k or v row, at element e, into the cache.  Every lane of the
+// warp calls it (Q8_0 shuffles within each block's lanes).
+template <Kind KIND, int N>
+__device__ __forceinline__ void put(const KvView &c, bool isk, int64_t row, int D, int e,
+                                    const float (&y)[N], bool write)
+{
+    uint8_t *dst = isk ? c.k : c.v;
+    if constexpr (KIND == kQ8) {
+        uint32_t codes[N / 4];
+        float d;
+        quantize<N>(y, codes, d);
+        if (write) {
+            if constexpr (N == 8)
+                *reinterpret_cast<uint2 *>(dst + row * D + e) = make_uint2(codes[0], codes[1]);
+            else
+                *reinterpret_cast<uint32_t *>(dst + row * D + e) = codes[0];
+            if (e % 32 == 0)
+                static_cast<__half *>(isk ? c.ks : c.vs)[row * kv_scales_per_row(D) + e / 32] =
+                    __float2half_rn(d);
+        }
+    } else if (write) {
+        if constexpr (KIND == kF16)
+            store_values<N>(reinterpret_cast<__half *>(dst) + row * D + e, y);
+        else
+            store_values<N>(reinterpret_cast<__nv_bfloat16 *>(dst) + row * D + e, y);
     }
+}
+
+// The usual shapes: a lane takes two chunks of a row that hold whole pairs
+// between them, so that nothing is loaded twice and no element asks what it
+// is: (u, u + half the rotated chunks) for halves, then consecutive chunks of
+// what passes through; (u, u + half the row's chunks) for adjacent pairs.
+template <Kind KIND, typename IO, int D>
+__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs P)
+{
+    constexpr int N = Chunk<IO>::N;
+    constexpr int LPR = D / N / 2;      // lanes per row
+    constexpr int RPW = 32 / LPR;       // rows per warp
+    constexpr int BATCH = 2;            // row groups under way at once
+    __shared__ __align__(16) float2 turn[128];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t tok = blockIdx.x;
+    const KvView &c = P.c;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int sub = lane / LPR, li = lane % LPR;
+    const int sub = lane / LPR, u = lane % LPR;
     const int rows = P.n_q + 2 * c.n_heads;
-    const bool vec = (P.n_rot & 7) == 0;
-    for (int base = (int(blockIdx.y) * kWarps + warp) * RPW; base < rows;
-         base += int(gridDim.y) * kWarps * RPW) {
-        const int r = base + sub;
+    const int stride = int(gridDim.y) * kWarps * RPW;
+    const int64_t slot = __ldg(P.slots + tok);
+    const IO *const qs = static_cast<const IO *>(P.q) + tok * P.ldq;
+    const IO *const ks = static_cast<const IO *>(P.k) + tok * P.ldk;
+    const IO *const vs = static_cast<const IO *>(P.v) + tok * P.ldv;
+    IO *const qd = static_cast<IO *>(P.q_out) + tok * P.ldqo;
+    // the lane's two chunks (first elements), and whether they turn
+    int ea, eb;
+    bool turn_a, turn_b;
+    const int hc = P.n_rot / 2 / N;  // chunks of half the rotated dims
+    if (P.adjacent || hc == 0) {
+        ea = u * N;
+        eb = (u + LPR) * N;
+        turn_a = ea < P.n_rot;
+        turn_b = eb < P.n_rot;
+    } else {
+        const int rest = u - hc;
+        ea = (rest < 0 ? u : 2 * hc + 2 * rest) * N;
+        eb = (rest < 0 ? u + hc : 2 * hc + 2 * rest + 1) * N;
+        turn_a = turn_b = rest < 0;
+    }
+    Chunk<IO> xa[BATCH], xb[BATCH];
+    auto load = [&](int base) {
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const int r = base + i * stride + sub;
+            const IO *src = r < P.n_q ? qs + r * D
+                            : r < P.n_q + c.n_heads ? ks + (r - P.n_q) * D
+                                                    : vs + (r - P.n_q - c.n_heads) * D;
+            if (sub < RPW && r < rows) {
+                xa[i].load(src + ea);
+                xb[i].load(src + eb);
+            } else {
+                xa[i].raw = xb[i].raw = make_uint4(0, 0, 0, 0);
+            }
+        }
+    };
+    int base = (int(blockIdx.y) * kWarps + warp) * RPW;
+    load(base);
+    turns_of(P, tok, turn);
+    const int64_t row0 = row_of_slot(P, slot);
+    __syncthreads();
+    while (base < rows) {
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const int r = base + i * stride + sub;
+            const bool isq = r < P.n_q, isk = !isq && r < P.n_q + c.n_heads;
+            const bool active = sub < RPW && r < rows;
+            float a[N], b[N];
+            xa[i].values(a);
+            xb[i].values(b);
+            if (isq || isk) {
+                if (P.adjacent) {
+                    auto pairs = [&](float (&x)[N], int e) {
+                        const float4 *cs = reinterpret_cast<const float4 *>(turn + e / 2);
+#pragma unroll
+                        for (int j = 0; j < N; j += 4) {
+                            const float4 w = cs[j / 4];
+                            const float x0 = x[j], x1 = x[j + 1], x2 = x[j + 2], x3 = x[j + 3];
+                            x[j] = __fsub_rn(__fmul_rn(x0, w.x), __fmul_rn(x1, w.y));
+                            x[j + 1] = __fadd_rn(__fmul_rn(x1, w.x), __fmul_rn(x0, w.y));
+                            x[j + 2] = __fsub_rn(__fmul_rn(x2, w.z), __fmul_rn(x3, w.w));
+                            x[j + 3] = __fadd_rn(__fmul_rn(x3, w.z), __fmul_rn(x2, w.w));
+                        }
+                    };
+                    if (turn_a)
+                        pairs(a, ea);
+                    if (turn_b)
+                        pairs(b, eb);
+                } else if (turn_a) {
+                    const float4 *cs = reinterpret_cast<const float4 *>(turn + ea);
+#pragma unroll
+                    for (int j = 0; j < N; j += 2) {
+                        const float4 w = cs[j / 2];
+                        const float a0 = a[j], a1 = a[j + 1], b0 = b[j], b1 = b[j + 1];
+                        a[j] = __fsub_rn(__fmul_rn(a0, w.x), __fmul_rn(b0, w.y));
+                        b[j] = __fadd_rn(__fmul_rn(b0, w.x), __fmul_rn(a0, w.y));
+                        a[j + 1] = __fsub_rn(__fmul_rn(a1, w.z), __fmul_rn(b1, w.w));
+                        b[j + 1] = __fadd_rn(__fmul_rn(b1, w.z), __fmul_rn(a1, w.w));
+                    }
+                }
+            }
+            if (isq) {  // (a row's loads are in registers: q_out may be q)
+                if (active) {
+                    store_values<N>(qd + r * D + ea, a);
+                    store_values<N>(qd + r * D + eb, b);
+                }
+            }
+            // (Q8_0's blocks of 32 are neighbouring lanes' first, or second, chunks)
+            if (KIND == kQ8 || !isq) {
+                const int head = isk ? r - P.n_q : r - P.n_q - c.n_heads;
+                const int64_t row = row0 + int64_t(head) * c.page_size;
+                const bool write = active && !isq && row0 >= 0;
+                put<KIND, N>(c, isk, row, D, ea, a, write);
+                put<KIND, N>(c, isk, row, D, eb, b, write);
+            }
+        }
+        base += BATCH * stride;
+        if (base < rows)
+            load(base);
+    }
+}
+
+// Any even number of rotated dims and any head size: a warp a row, every
+// element looks up its partner.
+template <Kind KIND, typename IO>
+__global__ void __launch_bounds__(kThreads) append_any_kernel(const __grid_constant__ AppendArgs P)
+{
+    constexpr int N = Chunk<IO>::N;
+    constexpr int PASSES = (256 / N + 31) / 32;
+    __shared__ __align__(16) float2 turn[128];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t tok = blockIdx.x;
+    const KvView &c = P.c;
+    const int D = c.D, half = P.n_rot >> 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rows = P.n_q + 2 * c.n_heads;
+    turns_of(P, tok, turn);
+    const int64_t row0 = row_of_slot(P, __ldg(P.slots + tok));
+    __syncthreads();
+    for (int r = int(blockIdx.y) * kWarps + warp; r < rows; r += int(gridDim.y) * kWarps) {
         const bool isq = r < P.n_q, isk = !isq && r < P.n_q + c.n_heads;
-        const bool active = sub < RPW && r < rows && (isq || stored);
         const int head = isq ? r : (isk ? r - P.n_q : r - P.n_q - c.n_heads);
         const IO *src = static_cast<const IO *>(isq ? P.q : (isk ? P.k : P.v)) +
                         tok * (isq ? P.ldq : (isk ? P.ldk : P.ldv)) + int64_t(head) * D;
-        const bool rot = isq || isk;
-        float4 own[PASSES], par[PASSES];
+        float y[PASSES][N];
 #pragma unroll
         for (int p = 0; p < PASSES; ++p) {
-            const int e = p * 128 + 4 * li;
-            own[p] = par[p] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (!active || e >= D)
-                continue;
-            own[p] = load4(src + e);
-            if (rot && !P.adjacent && e < P.n_rot) {
-                if (vec) {
-                    par[p] = load4(src + (e < half ? e + half : e - half));
-                } else {
-                    float *f = reinterpret_cast<float *>(&par[p]);
+            const int e = (p * 32 + lane) * N;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (e + j < P.n_rot)
-                            f[j] = load1(src + (e + j < half ? e + j + half : e + j - half));
+            for (int j = 0; j < N; ++j) {
+                y[p][j] = 0.f;
+                if (e >= D)
+                    continue;
+                const float x = load1(src + e + j);
+                y[p][j] = x;
+                if ((isq || isk) && e + j < P.n_rot) {
+                    const bool second = P.adjacent ? (j & 1) : e + j >= half;
+                    const int pair = P.adjacent ? (e + j) >> 1 : (second ? e + j - half : e + j);
+                    const int at = P.adjacent ? (e + j) ^ 1 : (second ? e + j - half : e + j + half);
+                    const float2 w = turn[pair];
+                    const float a = __fmul_rn(x, w.x), b = __fmul_rn(load1(src + at), w.y);
+                    y[p][j] = second ? __fadd_rn(a, b) : __fsub_rn(a, b);
                 }
             }
         }
         __syncwarp();  // q_out may be q: every load of the row is done before its first store
 #pragma unroll
         for (int p = 0; p < PASSES; ++p) {
-            const int e = p * 128 + 4 * li;
-            const bool here = active && e < D;
-            float4 y = own[p];
-            if (here && rot && e < P.n_rot) {
-                const float *x = reinterpret_cast<const float *>(&own[p]);
-                const float *o = reinterpret_cast<const float *>(&par[p]);
-                float *f = reinterpret_cast<float *>(&y);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (e + j >= P.n_rot)
-                        continue;
-                    const bool second = P.adjacent ? (j & 1) : e + j >= half;
-                    const int pair = P.adjacent ? (e + j) >> 1 : (second ? e + j - half : e + j);
-                    const float other = P.adjacent ? x[j ^ 1] : o[j];
-                    const float2 cs = turn[pair];
-                    const float a = __fmul_rn(x[j], cs.x), b = __fmul_rn(other, cs.y);
-                    f[j] = second ? __fadd_rn(a, b) : __fsub_rn(a, b);
-                }
-            }
-            if (here && isq)
-                store4(static_cast<IO *>(P.q_out) + tok * P.ldqo + int64_t(head) * D + e, y);
-            const int64_t row = row0 + int64_t(head) * c.page_size;
-            uint8_t *dst = (isk ? c.k : c.v);
-            if constexpr (KIND == kQ8) {
-                float d;
-                const uint32_t codes = quantize4(y, d);  // (every lane: it shuffles)
-                if (here && !isq) {
-                    *reinterpret_cast<uint32_t *>(dst + row * D + e) = codes;
-                    if ((lane & 7) == 0)
-                        static_cast<__half *>(isk ? c.ks : c.vs)[row * SP + e / 32] =
-                            __float2half_rn(d);
-                }
-            } else if (here && !isq) {
-                if constexpr (KIND == kF16)
-                    store4(reinterpret_cast<__half *>(dst) + row * D + e, y);
-                else
-                    store4(reinterpret_cast<__nv_bfloat16 *>(dst) + row * D + e, y);
+            const int e = (p * 32 + lane) * N;
+            if (isq) {
+                if (e < D)
+                    store_values<N>(static_cast<IO *>(P.q_out) + tok * P.ldqo + int64_t(head) * D +
+                                        e, y[p]);
+            } else {
+                put<KIND, N>(c, isk, row0 + int64_t(head) * c.page_size, D, e, y[p],
+                             e < D && row0 >= 0);
             }
         }
     }
 }
 
-// Rows of the cache as values: a thread takes four values of k and of v.
+// Rows of the cache as values.  A block takes a few consecutive tokens: it
+// finds their rows once, then its threads walk chunks of eight values of k
+// and of v, several under way at once.
+constexpr int kReadValues = 8;
+constexpr int kReadTokens = 64;  // at most
+
 template <Kind KIND, typename IO>
 __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ KvReadArgs P)
 {
+    __shared__ uint32_t row_of[kReadTokens];  // row of head 0; ~0 for none
     pdl_wait();
     pdl_launch_dependents();
     const KvView &c = P.c;
-    const int D = c.D, quads = D / 4, SP = kv_scales_per_row(D);
-    const int per_token = c.n_heads * quads;
-    const int64_t n = P.T * per_token;
-    for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < n;
-         i += int64_t(gridDim.x) * kThreads) {
-        const int64_t tok = i / per_token;
-        const int in = int(i - tok * per_token);
-        const int head = in / quads, e = (in - head * quads) * 4;
-        const int64_t slot = __ldg(P.slots + tok);
+    const int D = c.D, SP = kv_scales_per_row(D);
+    const int64_t tok0 = int64_t(blockIdx.x) * P.tokens;
+    const int n = int(min(int64_t(P.tokens), P.T - tok0));
+    if (int(threadIdx.x) < n) {
+        const int64_t slot = __ldg(P.slots + tok0 + threadIdx.x);
         const bool held = slot >= 0 && slot < int64_t(c.n_pages) * c.page_size;
-        if (slot >= 0 && !held && in == 0)
+        if (slot >= 0 && !held)
             atomicOr(P.status, kStatusBadSlotBit);
-        float4 kv[2] = {};
+        uint32_t row = ~0u;
         if (held) {
             const int64_t page = slot / c.page_size;
-            const int64_t row =
-                (page * c.n_heads + head) * c.page_size + (slot - page * c.page_size);
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                if (!(w ? P.v : P.k))
-                    continue;
-                const uint8_t *src = w ? c.v : c.k;
-                if constexpr (KIND == kF16) {
-                    kv[w] = load4(reinterpret_cast<const __half *>(src) + row * D + e);
-                } else if constexpr (KIND == kBF16) {
-                    kv[w] = load4(reinterpret_cast<const __nv_bfloat16 *>(src) + row * D + e);
-                } else {
-                    const char4 q = *reinterpret_cast<const char4 *>(src + row * D + e);
-                    const float d = __half2float(
-                        static_cast<const __half *>(w ? c.vs : c.ks)[row * SP + e / 32]);
-                    kv[w] = make_float4(q.x * d, q.y * d, q.z * d, q.w * d);
-                }
-            }
+            row = uint32_t(page * c.n_heads * c.page_size + (slot - page * c.page_size));
         }
-        if (P.k)
-            store4(static_cast<IO *>(P.k) + tok * P.ldk + int64_t(head) * D + e, kv[0]);
-        if (P.v)
-            store4(static_cast<IO *>(P.v) + tok * P.ldv + int64_t(head) * D + e, kv[1]);
+        row_of[threadIdx.x] = row;
+    }
+    __syncthreads();
+    const int units = n * int(P.unit.d);
+#pragma unroll 4
+    for (int i = threadIdx.x; i < units; i += kThreads) {
+        const int t = int(fast_div(P.unit, unsigned(i)));
+        const int in = i - t * int(P.unit.d);
+        const int head = int(fast_div(P.chunk, unsigned(in)));
+        const int e = (in - head * int(P.chunk.d)) * kReadValues;
+        const uint32_t row0 = row_of[t];
+        const bool held = row0 != ~0u;
+        const uint64_t row = held ? uint64_t(row0) + unsigned(head) * unsigned(c.page_size) : 0;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            IO *out = static_cast<IO *>(w ? P.v : P.k);
+            if (!out)
+                continue;
+            const uint8_t *src = w ? c.v : c.k;
+            float v[kReadValues];
+            if constexpr (KIND == kQ8) {
+                const uint2 q = __ldg(reinterpret_cast<const uint2 *>(src + row * D + e));
+                const float d =
+                    __half2float(__ldg(static_cast<const __half *>(w ? c.vs : c.ks) + row * SP +
+                                       e / 32));
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[j] = float(int(int8_t((j < 4 ? q.x : q.y) >> (8 * (j & 3))))) * d;
+            } else {
+                using H = typename std::conditional<KIND == kBF16, __nv_bfloat16, __half>::type;
+                Chunk<H> ch;
+                ch.load(reinterpret_cast<const H *>(src) + row * D + e);
+                ch.values(v);
+            }
+            if (!held) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[j] = 0.f;
+            }
+            store_values<8>(out + (tok0 + t) * (w ? P.ldv : P.ldk) + int64_t(head) * D + e, v);
+        }
     }
 }
 
@@ -226,9 +426,32 @@ cudaError_t launch(void (*k)(Args), dim3 grid, cudaStream_t s, const Args &a)
     return counted(cudaLaunchKernelEx(&cfg, k, a));
 }
 
-template <Kind KIND, typename IO>
-cudaError_t append_for_dim(const AppendArgs &a, dim3 grid, cudaStream_t s)
+// Whether append_kernel's lanes hold whole pairs, and whole Q8_0 blocks are
+// neighbouring lanes.
+template <Kind KIND, int N>
+bool append_regular(const AppendArgs &a)
 {
+    const int D = a.c.D;
+    if (a.adjacent ? a.n_rot % N != 0 : a.n_rot % (2 * N) != 0)
+        return false;
+    if (KIND != kQ8)
+        return true;
+    return D % 64 == 0 && (a.adjacent || a.n_rot == 0 || a.n_rot == D);
+}
+
+template <Kind KIND, typename IO>
+cudaError_t append_for_dim(const AppendArgs &a, int sm_count, cudaStream_t s)
+{
+    constexpr int N = Chunk<IO>::N;
+    const bool regular = append_regular<KIND, N>(a);
+    // Few tokens: a block takes as few heads as keep about four blocks on
+    // every SM; from there on a block takes the whole token.
+    const int rows = kWarps * (regular ? 32 / (a.c.D / N / 2) : 1);  // of a block at a time
+    const int passes = (a.n_q + 2 * a.c.n_heads + rows - 1) / rows;
+    const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(passes, 4 * sm_count / a.T));
+    const dim3 grid(unsigned(a.T), unsigned(parts));
+    if (!regular)
+        return launch(append_any_kernel<KIND, IO>, grid, s, a);
     switch (a.c.D) {
     case 64: return launch(append_kernel<KIND, IO, 64>, grid, s, a);
     case 96: return launch(append_kernel<KIND, IO, 96>, grid, s, a);
@@ -240,12 +463,12 @@ cudaError_t append_for_dim(const AppendArgs &a, dim3 grid, cudaStream_t s)
 }
 
 template <Kind KIND>
-cudaError_t append_for_io(const AppendArgs &a, dim3 grid, cudaStream_t s)
+cudaError_t append_for_io(const AppendArgs &a, int sm_count, cudaStream_t s)
 {
     switch (a.dtype) {
-    case QMM_F32: return append_for_dim<KIND, float>(a, grid, s);
-    case QMM_F16: return append_for_dim<KIND, __half>(a, grid, s);
-    case QMM_BF16: return append_for_dim<KIND, __nv_bfloat16>(a, grid, s);
+    case QMM_F32: return append_for_dim<KIND, float>(a, sm_count, s);
+    case QMM_F16: return append_for_dim<KIND, __half>(a, sm_count, s);
+    case QMM_BF16: return append_for_dim<KIND, __nv_bfloat16>(a, sm_count, s);
     }
     return cudaErrorInvalidValue;
 }
@@ -265,24 +488,25 @@ cudaError_t read_for_io(const KvReadArgs &a, dim3 grid, cudaStream_t s)
 
 cudaError_t launch_kv_append(const AppendArgs &a, int sm_count, cudaStream_t s)
 {
-    // Few tokens: a block takes as few heads as keep about four blocks on
-    // every SM; from there on a block takes the whole token.
-    const int rpw = a.c.D <= 64 ? 2 : 1;
-    const int passes = (a.n_q + 2 * a.c.n_heads + kWarps * rpw - 1) / (kWarps * rpw);
-    const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(passes, 4 * sm_count / a.T));
-    const dim3 grid(unsigned(a.T), unsigned(parts));
     switch (a.type) {
-    case QMM_F16: return append_for_io<kF16>(a, grid, s);
-    case QMM_BF16: return append_for_io<kBF16>(a, grid, s);
-    default: return append_for_io<kQ8>(a, grid, s);
+    case QMM_F16: return append_for_io<kF16>(a, sm_count, s);
+    case QMM_BF16: return append_for_io<kBF16>(a, sm_count, s);
+    default: return append_for_io<kQ8>(a, sm_count, s);
     }
 }
 
-cudaError_t launch_kv_read(const KvReadArgs &a, int sm_count, cudaStream_t s)
+cudaError_t launch_kv_read(const KvReadArgs &args, int sm_count, cudaStream_t s)
 {
-    const int64_t n = a.T * a.c.n_heads * (a.c.D / 4);
-    const int64_t want = (n + kThreads - 1) / kThreads;
-    const dim3 grid(unsigned(std::min<int64_t>(want, int64_t(sm_count) * 16)));
+    KvReadArgs a = args;
+    const int64_t units = int64_t(a.c.n_heads) * (a.c.D / kReadValues);  // of a token
+    a.unit = make_fast_div(uint32_t(units));
+    a.chunk = make_fast_div(uint32_t(a.c.D / kReadValues));
+    // tokens of a block: about four chunks of k and of v a thread, fewer while
+    // there are SMs without a block
+    a.tokens = int(std::max<int64_t>(
+        1, std::min({int64_t(4 * kThreads) / units, (a.T + sm_count - 1) / sm_count,
+                     int64_t(kReadTokens)})));
+    const dim3 grid(unsigned((a.T + a.tokens - 1) / a.tokens));
     switch (a.type) {
     case QMM_F16: return read_for_io<kF16>(a, grid, s);
     case QMM_BF16: return read_for_io<kBF16>(a, grid, s);

@@ -60,6 +60,14 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16)
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
+__device__ __forceinline__ float2 unpack2(uint32_t u, __half)
+{
+    return __half22float2(*reinterpret_cast<const __half2 *>(&u));
+}
+__device__ __forceinline__ float2 unpack2(uint32_t u, __nv_bfloat16)
+{
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
 __device__ __forceinline__ void store4(float *p, float4 v)
 {
     *reinterpret_cast<float4 *>(p) = v;

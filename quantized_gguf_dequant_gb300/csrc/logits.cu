@@ -28,6 +28,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr uint32_t kNoOwner = 0xffffffffu;
+constexpr int WIDE = 4;   // groups of four logits of a thread where rows are many
+constexpr int AHEAD = 4;  // history tokens of a thread under way at once
 
 __device__ __forceinline__ int64_t clamp64(int64_t v, int64_t hi)
 {
@@ -49,13 +51,15 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const __grid_constant_
     IO *out = static_cast<IO *>(P.out) + b * P.ld_out;
     // logits before the row's first group boundary
     const int shift = VEC ? int((reinterpret_cast<uintptr_t>(in) / sizeof(IO)) & 3) : 0;
-    const int64_t v0 = int64_t(blockIdx.y) * CHUNK - shift;
+    const int v0 = int(blockIdx.y) * CHUNK - shift;  // (n_vocab <= 2^26)
     const int V = int(P.V), tid = threadIdx.x;
 
+    // Everything whose place is known is asked for at once: the logits, the
+    // mask's words, the lists' ends and the penalties.
     float4 x[GROUPS];
 #pragma unroll
     for (int i = 0; i < GROUPS; ++i) {
-        const int64_t e = v0 + (i * kThreads + tid) * 4;
+        const int e = v0 + (i * kThreads + tid) * 4;
         x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (VEC && e >= 0 && e + 4 <= V) {
             x[i] = load4(in + e);
@@ -67,18 +71,44 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const __grid_constant_
                     f[j] = load1(in + e + j);
         }
     }
-
+    uint32_t word[GROUPS];
+    const uint32_t *mask = P.mask ? P.mask + b * P.ld_mask : nullptr;
+#pragma unroll
+    for (int i = 0; i < GROUPS; ++i) {
+        const int e = v0 + (i * kThreads + tid) * 4;
+        word[i] = mask && e < V ? __ldg(mask + (e < 0 ? 0 : e >> 5)) : 0u;
+    }
     int64_t h0 = 0, h1 = 0, b0 = 0, b1 = 0;
     if (P.n_history > 0) {
-        h0 = clamp64(P.history_offsets[b], P.n_history);
-        h1 = clamp64(P.history_offsets[b + 1], P.n_history);
+        h0 = clamp64(__ldg(P.history_offsets + b), P.n_history);
+        h1 = clamp64(__ldg(P.history_offsets + b + 1), P.n_history);
     }
     if (P.n_biases > 0) {
-        b0 = clamp64(P.bias_offsets[b], P.n_biases);
-        b1 = clamp64(P.bias_offsets[b + 1], P.n_biases);
+        b0 = clamp64(__ldg(P.bias_offsets + b), P.n_biases);
+        b1 = clamp64(__ldg(P.bias_offsets + b + 1), P.n_biases);
     }
+    const float r = P.repeat ? __ldg(P.repeat + b) : 1.f;
+    const float presence = P.presence ? __ldg(P.presence + b) : 0.f;
+    const float frequency = P.frequency ? __ldg(P.frequency + b) : 0.f;
     const bool counted = h1 > h0, biased = b1 > b0;
     if (counted || biased) {
+        // a token's place in this chunk, or -1
+        auto place = [&](int id) {
+            const unsigned at = unsigned(id) - unsigned(v0);
+            return unsigned(id) < unsigned(V) && at < unsigned(CHUNK) ? int(at) : -1;
+        };
+        // the first of the lists are on their way while the arrays are cleared
+        int id[AHEAD], bid = -1;
+        float bval = 0.f;
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            const int64_t i = h0 + tid + j * kThreads;
+            id[j] = i < h1 ? __ldg(P.history + i) : -1;
+        }
+        if (b0 + tid < b1) {
+            bid = __ldg(P.bias_ids + b0 + tid);
+            bval = __ldg(P.bias_values + b0 + tid);
+        }
 #pragma unroll
         for (int i = 0; i < GROUPS; ++i) {
             const int at = (i * kThreads + tid) * 4;
@@ -89,44 +119,50 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const __grid_constant_
                     make_uint4(kNoOwner, kNoOwner, kNoOwner, kNoOwner);
         }
         __syncthreads();
-        // a token's place in this chunk, or -1
-        auto place = [&](int id) {
-            const int64_t at = int64_t(id) - v0;
-            return id >= 0 && id < V && at >= 0 && at < CHUNK ? int(at) : -1;
-        };
-#pragma unroll 4
-        for (int64_t i = h0 + tid; i < h1; i += kThreads) {
-            const int at = place(__ldg(P.history + i));
-            if (at >= 0)
-                atomicAdd(counts + at, 1u);
+        for (int64_t i = h0 + tid; i < h1; i += AHEAD * kThreads) {
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {
+                const int at = place(id[j]);
+                if (at >= 0)
+                    atomicAdd(counts + at, 1u);
+                const int64_t next = i + (AHEAD + j) * kThreads;
+                id[j] = next < h1 ? __ldg(P.history + next) : -1;
+            }
         }
         if (biased) {
-            for (int64_t i = b0 + tid; i < b1; i += kThreads) {
-                const int at = place(__ldg(P.bias_ids + i));
-                if (at >= 0)
-                    atomicMin(bias + at, uint32_t(i - b0));
+            int at = place(bid);
+            if (at >= 0)
+                atomicMin(bias + at, uint32_t(tid));
+            for (int64_t i = b0 + tid + kThreads; i < b1; i += kThreads) {
+                const int a2 = place(__ldg(P.bias_ids + i));
+                if (a2 >= 0)
+                    atomicMin(bias + a2, uint32_t(i - b0));
             }
             __syncthreads();
-            bool twice = false;  // does the list name a token of this chunk twice?
-            for (int64_t i = b0 + tid; i < b1; i += kThreads) {
-                const int at = place(__ldg(P.bias_ids + i));
-                twice |= at >= 0 && bias[at] != uint32_t(i - b0);
+            bool twice = at >= 0 && bias[at] != uint32_t(tid);  // a token of this chunk named twice
+            for (int64_t i = b0 + tid + kThreads; i < b1; i += kThreads) {
+                const int a2 = place(__ldg(P.bias_ids + i));
+                twice |= a2 >= 0 && bias[a2] != uint32_t(i - b0);
             }
             twice = __syncthreads_or(twice);
             for (int64_t i = b0 + tid; i < b1; i += kThreads) {
-                const int id = __ldg(P.bias_ids + i), at = place(id);
+                if (i >= b0 + kThreads) {
+                    bid = __ldg(P.bias_ids + i);
+                    bval = __ldg(P.bias_values + i);
+                    at = place(bid);
+                }
                 if (at < 0)
                     continue;
-                float sum = __ldg(P.bias_values + i);
+                float sum = bval;
                 if (twice) {
                     // (the owners' indices are being overwritten: look at the list)
                     int64_t k = b0;
-                    while (k < i && __ldg(P.bias_ids + k) != id)
+                    while (k < i && __ldg(P.bias_ids + k) != bid)
                         ++k;
                     if (k < i)
                         continue;
                     for (k = i + 1; k < b1; ++k)
-                        if (__ldg(P.bias_ids + k) == id)
+                        if (__ldg(P.bias_ids + k) == bid)
                             sum = __fadd_rn(sum, __ldg(P.bias_values + k));
                 }
                 const uint32_t bits = __float_as_uint(sum);
@@ -135,46 +171,45 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const __grid_constant_
         }
         __syncthreads();
     }
-    const float r = P.repeat ? __ldg(P.repeat + b) : 1.f;
-    const float presence = P.presence ? __ldg(P.presence + b) : 0.f;
-    const float frequency = P.frequency ? __ldg(P.frequency + b) : 0.f;
-    const uint32_t *mask = P.mask ? P.mask + b * P.ld_mask : nullptr;
 #pragma unroll
     for (int i = 0; i < GROUPS; ++i) {
         const int at = (i * kThreads + tid) * 4;
-        const int64_t e = v0 + at;
+        const int e = v0 + at;
         if (e + 4 <= 0 || e >= V)
             continue;
         float *f = reinterpret_cast<float *>(&x[i]);
         if (counted) {
             const uint4 c4 = *reinterpret_cast<const uint4 *>(counts + at);
-            const uint32_t c[4] = {c4.x, c4.y, c4.z, c4.w};
+            if (c4.x | c4.y | c4.z | c4.w) {
+                const uint32_t c[4] = {c4.x, c4.y, c4.z, c4.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (c[j]) {
-                    const float z = f[j] > 0.f ? __fdiv_rn(f[j], r) : __fmul_rn(f[j], r);
-                    f[j] = __fsub_rn(z, __fadd_rn(presence, __fmul_rn(frequency, float(c[j]))));
-                }
+                for (int j = 0; j < 4; ++j)
+                    if (c[j]) {
+                        const float z = f[j] > 0.f ? __fdiv_rn(f[j], r) : __fmul_rn(f[j], r);
+                        f[j] =
+                            __fsub_rn(z, __fadd_rn(presence, __fmul_rn(frequency, float(c[j]))));
+                    }
+            }
         }
         if (biased) {
             const uint4 s4 = *reinterpret_cast<const uint4 *>(bias + at);
-            const uint32_t s[4] = {s4.x, s4.y, s4.z, s4.w};
+            if ((s4.x & s4.y & s4.z & s4.w) != kNoOwner) {
+                const uint32_t s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (s[j] != kNoOwner)
-                    f[j] = __fadd_rn(f[j], __uint_as_float(s[j]));
+                for (int j = 0; j < 4; ++j)
+                    if (s[j] != kNoOwner)
+                        f[j] = __fadd_rn(f[j], __uint_as_float(s[j]));
+            }
         }
         if (mask) {
-            const int first = int(e < 0 ? 0 : e), w = first >> 5;
-            const uint32_t lo = __ldg(mask + w);
-            const uint32_t hi = (w + 1) * 32 < V ? __ldg(mask + w + 1) : 0u;
-            const uint32_t bits = __funnelshift_r(lo, hi, first & 31);
+            const int first = e < 0 ? 0 : e, w = first >> 5;
+            // (groups at odd places may reach into the next word)
+            const uint32_t hi = (first & 31) > 28 && (w + 1) * 32 < V ? __ldg(mask + w + 1) : 0u;
+            const uint32_t bits = __funnelshift_r(word[i], hi, first & 31);
+            const uint32_t four = e < 0 ? bits << -e : bits;  // bit j: logit e + j
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int bit = int(e + j) - first;
-                if (bit >= 0 && !((bits >> bit) & 1u))
-                    f[j] = -INFINITY;
-            }
+            for (int j = 0; j < 4; ++j)
+                f[j] = four & (1u << j) ? f[j] : -INFINITY;
         }
         if (VEC && e >= 0 && e + 4 <= V) {
             store4(out + e, x[i]);
@@ -220,7 +255,7 @@ cudaError_t launch_io(const LogitsArgs &a, int sm_count, cudaStream_t s)
     // over the SMs.
     const bool wide = a.B * a.V >= int64_t(sm_count) * 4 * 8192;
     if (wide)
-        return vec ? launch<IO, 8, true>(a, s) : launch<IO, 8, false>(a, s);
+        return vec ? launch<IO, WIDE, true>(a, s) : launch<IO, WIDE, false>(a, s);
     return vec ? launch<IO, 2, true>(a, s) : launch<IO, 2, false>(a, s);
 }
 

@@ -442,6 +442,9 @@ struct KvReadArgs {
     void *k, *v;                  // either may be null
     int64_t ldk, ldv;
     unsigned *status;
+    // set by the launcher: chunks of a token and of a row, tokens of a block
+    FastDiv unit, chunk;
+    int tokens;
 };
 cudaError_t launch_kv_read(const KvReadArgs &a, int sm_count, cudaStream_t s);
 
