@@ -27,6 +27,9 @@ namespace qmm {
 
 namespace {
 
+#ifndef APPEND_BLOCKS
+#define APPEND_BLOCKS 4
+#endif
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
@@ -164,7 +167,7 @@ __device__ __forceinline__ void put(const KvView &c, bool isk, int64_t row, int 
 // is: (u, u + half the rotated chunks) for halves, then consecutive chunks of
 // what passes through; (u, u + half the row's chunks) for adjacent pairs.
 template <Kind KIND, typename IO, int D>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs P)
+__global__ void __launch_bounds__(kThreads, APPEND_BLOCKS) append_kernel(const __grid_constant__ AppendArgs P)
 {
     constexpr int N = Chunk<IO>::N;
     constexpr int LPR = D / N / 2;      // lanes per row
@@ -342,14 +345,16 @@ __global__ void __launch_bounds__(kThreads) append_any_kernel(const __grid_const
 }
 
 // Rows of the cache as values.  A block takes a few consecutive tokens: it
-// finds their rows once, then its threads walk chunks of eight values of k
-// and of v, several under way at once.
-constexpr int kReadValues = 8;
-constexpr int kReadTokens = 64;  // at most
+// finds their rows once, then every thread asks for all its chunks of k and of
+// v before it converts the first.  A chunk is what 16 bytes of output hold.
+constexpr int kReadTokens = 64;  // of a block, at most
+constexpr int kReadUnits = 4;    // chunks of a thread under way at once
 
 template <Kind KIND, typename IO>
 __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ KvReadArgs P)
 {
+    constexpr int N = Chunk<IO>::N;
+    using H = typename std::conditional<KIND == kBF16, __nv_bfloat16, __half>::type;
     __shared__ uint32_t row_of[kReadTokens];  // row of head 0; ~0 for none
     pdl_wait();
     pdl_launch_dependents();
@@ -364,49 +369,91 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
             atomicOr(P.status, kStatusBadSlotBit);
         uint32_t row = ~0u;
         if (held) {
-            const int64_t page = slot / c.page_size;
-            row = uint32_t(page * c.n_heads * c.page_size + (slot - page * c.page_size));
+            const uint32_t page = slot < 0x7fffffff
+                                      ? fast_div(c.page, uint32_t(slot))
+                                      : uint32_t(uint64_t(slot) / uint32_t(c.page_size));
+            row = page * uint32_t(c.n_heads) * uint32_t(c.page_size) +
+                  uint32_t(slot - int64_t(page) * c.page_size);
         }
         row_of[threadIdx.x] = row;
     }
     __syncthreads();
     const int units = n * int(P.unit.d);
-#pragma unroll 4
-    for (int i = threadIdx.x; i < units; i += kThreads) {
-        const int t = int(fast_div(P.unit, unsigned(i)));
-        const int in = i - t * int(P.unit.d);
-        const int head = int(fast_div(P.chunk, unsigned(in)));
-        const int e = (in - head * int(P.chunk.d)) * kReadValues;
-        const uint32_t row0 = row_of[t];
-        const bool held = row0 != ~0u;
-        const uint64_t row = held ? uint64_t(row0) + unsigned(head) * unsigned(c.page_size) : 0;
+    for (int i0 = threadIdx.x; i0 < units; i0 += kReadUnits * kThreads) {
+        uint2 raw[2][kReadUnits] = {};  // 4 or 8 codes, or 4 values of 16 bits
+        uint2 more[2][kReadUnits] = {}; // 8 values of 16 bits: the second half
+        __half scale[2][kReadUnits];
+        int64_t at[kReadUnits];         // token
+        int off[kReadUnits];            // element within the token
+        bool held[kReadUnits];
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            IO *out = static_cast<IO *>(w ? P.v : P.k);
-            if (!out)
+        for (int u = 0; u < kReadUnits; ++u) {
+            const int i = min(i0 + u * kThreads, units - 1);
+            const int t = int(fast_div(P.unit, unsigned(i)));
+            const int in = i - t * int(P.unit.d);
+            const int head = int(fast_div(P.chunk, unsigned(in)));
+            const int e = (in - head * int(P.chunk.d)) * N;
+            const uint32_t row0 = row_of[t];
+            held[u] = row0 != ~0u;
+            at[u] = tok0 + t;
+            off[u] = head * D + e;
+            const uint64_t row =
+                held[u] ? uint64_t(row0) + unsigned(head) * unsigned(c.page_size) : 0;
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                if (!(w ? P.v : P.k))
+                    continue;
+                const uint8_t *src = w ? c.v : c.k;
+                if constexpr (KIND == kQ8) {
+                    if constexpr (N == 8)
+                        raw[w][u] = __ldg(reinterpret_cast<const uint2 *>(src + row * D + e));
+                    else
+                        raw[w][u].x = __ldg(reinterpret_cast<const uint32_t *>(src + row * D + e));
+                    scale[w][u] =
+                        __ldg(static_cast<const __half *>(w ? c.vs : c.ks) + row * SP + e / 32);
+                } else {
+                    const H *p = reinterpret_cast<const H *>(src) + row * D + e;
+                    if constexpr (N == 8) {
+                        const uint4 q = __ldg(reinterpret_cast<const uint4 *>(p));
+                        raw[w][u] = make_uint2(q.x, q.y);
+                        more[w][u] = make_uint2(q.z, q.w);
+                    } else {
+                        raw[w][u] = __ldg(reinterpret_cast<const uint2 *>(p));
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kReadUnits; ++u) {
+            if (i0 + u * kThreads >= units)
                 continue;
-            const uint8_t *src = w ? c.v : c.k;
-            float v[kReadValues];
-            if constexpr (KIND == kQ8) {
-                const uint2 q = __ldg(reinterpret_cast<const uint2 *>(src + row * D + e));
-                const float d =
-                    __half2float(__ldg(static_cast<const __half *>(w ? c.vs : c.ks) + row * SP +
-                                       e / 32));
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[j] = float(int(int8_t((j < 4 ? q.x : q.y) >> (8 * (j & 3))))) * d;
-            } else {
-                using H = typename std::conditional<KIND == kBF16, __nv_bfloat16, __half>::type;
-                Chunk<H> ch;
-                ch.load(reinterpret_cast<const H *>(src) + row * D + e);
-                ch.values(v);
-            }
-            if (!held) {
+            for (int w = 0; w < 2; ++w) {
+                IO *out = static_cast<IO *>(w ? P.v : P.k);
+                if (!out)
+                    continue;
+                float v[N];
+                const uint32_t q[4] = {raw[w][u].x, raw[w][u].y, more[w][u].x, more[w][u].y};
+                if constexpr (KIND == kQ8) {
+                    const float d = __half2float(scale[w][u]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[j] = 0.f;
+                    for (int j = 0; j < N; ++j)
+                        v[j] = float(int(int8_t(q[j / 4] >> (8 * (j & 3))))) * d;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < N; j += 2) {
+                        const float2 f = unpack2(q[j / 2], H());
+                        v[j] = f.x;
+                        v[j + 1] = f.y;
+                    }
+                }
+                if (!held[u]) {
+#pragma unroll
+                    for (int j = 0; j < N; ++j)
+                        v[j] = 0.f;
+                }
+                store_values<N>(out + at[u] * (w ? P.ldv : P.ldk) + off[u], v);
             }
-            store_values<8>(out + (tok0 + t) * (w ? P.ldv : P.ldk) + int64_t(head) * D + e, v);
         }
     }
 }
@@ -498,13 +545,14 @@ cudaError_t launch_kv_append(const AppendArgs &a, int sm_count, cudaStream_t s)
 cudaError_t launch_kv_read(const KvReadArgs &args, int sm_count, cudaStream_t s)
 {
     KvReadArgs a = args;
-    const int64_t units = int64_t(a.c.n_heads) * (a.c.D / kReadValues);  // of a token
+    const int n = a.dtype == QMM_F32 ? 4 : 8;                    // values of a chunk
+    const int64_t units = int64_t(a.c.n_heads) * (a.c.D / n);    // of a token
     a.unit = make_fast_div(uint32_t(units));
-    a.chunk = make_fast_div(uint32_t(a.c.D / kReadValues));
-    // tokens of a block: about four chunks of k and of v a thread, fewer while
-    // there are SMs without a block
+    a.chunk = make_fast_div(uint32_t(a.c.D / n));
+    // tokens of a block: what its threads ask for at once, fewer while there
+    // are SMs without a block
     a.tokens = int(std::max<int64_t>(
-        1, std::min({int64_t(4 * kThreads) / units, (a.T + sm_count - 1) / sm_count,
+        1, std::min({int64_t(kReadUnits * kThreads) / units, (a.T + sm_count - 1) / sm_count,
                      int64_t(kReadTokens)})));
     const dim3 grid(unsigned((a.T + a.tokens - 1) / a.tokens));
     switch (a.type) {

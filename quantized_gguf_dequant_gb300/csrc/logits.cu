@@ -1,5 +1,5 @@
 // logits.cu -- a model's logits adjusted before sampling: penalties for
-// repeated tokens, biases, and a mask of what a grammar allows, in one pass.
+// repeated tokens, biases, and a mask of what a grammar allows, in one launch.
 //
 //   c = times v occurs in the row's history
 //   z = logits[v];  c > 0:  z = z > 0 ? z / r : z * r;  z -= presence + frequency * c
@@ -7,16 +7,22 @@
 //   bit v of the row's mask clear:  z = -inf
 // all in fp32, rounded once to the logits' type.
 //
-// Bytes bound it: each logit is read and written once.  A block owns a chunk
-// of one row: it takes the chunk's logits into registers, counts the history
-// tokens that fall into the chunk in shared memory (whole-number atomics: no
-// order to matter) while those loads are under way, and applies everything on
-// the way out.  The history is scanned by every chunk of its row, out of L2.
+// Bytes bound it: each logit is read and written once.  A block takes a part
+// of a row.  First it streams the part from input to output, 16 bytes a lane,
+// under the mask alone; a call in place without a mask skips this, and its
+// time no longer depends on the vocabulary's size.  Few logits are named by
+// the history or a bias (a thousand or two of a hundred thousand), so these are
+// done on their own: a bitmap of the part's named tokens, counts by their rank
+// in it (whole-number atomics: no order to matter), then one thread a token,
+// which computes from the input.  Testing every logit against dense counts
+// instead takes three times the instructions of the stream itself and was
+// bound by issuing them (256 rows of 128256 logits: 67 us).
 // A bias list may name a token twice: the entry with the lowest index owns
 // the token and adds the others in list order, so the sum is repeatable.
-// Groups of four logits are taken at their 16-byte boundaries whatever the
-// row's own alignment, so an odd vocabulary costs nothing but its ragged ends.
+// Groups are taken at their 16-byte boundaries whatever the row's own
+// alignment, so an odd vocabulary costs nothing but its ragged ends.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv_cache.cuh"
 #include "qmm_device.cuh"
@@ -27,57 +33,120 @@ namespace qmm {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kLongest = 16384;    // logits of a part, at most
+constexpr int kAhead = 8;          // history tokens that a thread keeps in registers
+constexpr int kWords = 2048;       // bitmap words of a window, at most
+constexpr int kPlaces = 1024;      // named tokens counted at once
 constexpr uint32_t kNoOwner = 0xffffffffu;
-constexpr int WIDE = 4;   // groups of four logits of a thread where rows are many
-constexpr int AHEAD = 4;  // history tokens of a thread under way at once
 
 __device__ __forceinline__ int64_t clamp64(int64_t v, int64_t hi)
 {
     return v < 0 ? 0 : (v > hi ? hi : v);
 }
 
-// VEC: input and output rows are equally misaligned, groups of four go as one.
-template <typename IO, int GROUPS, bool VEC>
-__global__ void __launch_bounds__(kThreads) adjust_kernel(const __grid_constant__ LogitsArgs P)
+// 32 mask bits from bit v on (those past the vocabulary are of no matter).
+__device__ __forceinline__ uint32_t mask_bits(const uint32_t *mask, int v, int V)
 {
-    constexpr int CHUNK = GROUPS * kThreads * 4;
-    extern __shared__ __align__(16) uint32_t shared[];
-    uint32_t *counts = shared;
-    uint32_t *bias = shared + (P.n_history > 0 ? CHUNK : 0);  // owner's index, then the sum's bits
-    pdl_wait();
-    pdl_launch_dependents();
-    const int64_t b = blockIdx.x;
-    const IO *in = static_cast<const IO *>(P.in) + b * P.ld_in;
-    IO *out = static_cast<IO *>(P.out) + b * P.ld_out;
-    // logits before the row's first group boundary
-    const int shift = VEC ? int((reinterpret_cast<uintptr_t>(in) / sizeof(IO)) & 3) : 0;
-    const int v0 = int(blockIdx.y) * CHUNK - shift;  // (n_vocab <= 2^26)
-    const int V = int(P.V), tid = threadIdx.x;
+    const int w = v >> 5, s = v & 31;
+    const uint32_t lo = __ldg(mask + w);
+    const uint32_t hi = s && (w + 1) * 32 < V ? __ldg(mask + w + 1) : 0u;
+    return __funnelshift_r(lo, hi, s);
+}
 
-    // Everything whose place is known is asked for at once: the logits, the
-    // mask's words, the lists' ends and the penalties.
-    float4 x[GROUPS];
+// The block's part [lo, hi) of a row from `in` to `out` under the mask.  VEC:
+// both rows are equally misaligned and lo is 0 or at a 16-byte boundary.
+template <typename IO, bool VEC>
+__device__ __forceinline__ void stream_part(const IO *in, IO *out, const uint32_t *mask, int lo,
+                                            int hi, int V)
+{
+    constexpr int N = 16 / sizeof(IO), DEEP = 4;
+    const int tid = threadIdx.x;
+    auto one = [&](int v) {
+        float z = load1(in + v);
+        if (mask && !(mask_bits(mask, v, V) & 1u))
+            z = -INFINITY;
+        store1(out + v, z);
+    };
+    if (!VEC) {
+        for (int v = lo + tid; v < hi; v += kThreads)
+            one(v);
+        return;
+    }
+    const int head = min(hi, lo + int((-(reinterpret_cast<uintptr_t>(in + lo) / sizeof(IO))) & (N - 1)));
+    const int groups = (hi - head) / N;
+    if (lo + tid < head)
+        one(lo + tid);
+    if (head + groups * N + tid < hi)
+        one(head + groups * N + tid);
+    const uint4 *src = reinterpret_cast<const uint4 *>(in + head);
+    uint4 *dst = reinterpret_cast<uint4 *>(out + head);
+    const bool odd = head % N != 0;  // groups may reach into a second mask word
+    for (int g0 = tid; g0 < groups; g0 += DEEP * kThreads) {
+        uint4 x[DEEP];
+        uint32_t word[DEEP], next[DEEP];
 #pragma unroll
-    for (int i = 0; i < GROUPS; ++i) {
-        const int e = v0 + (i * kThreads + tid) * 4;
-        x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (VEC && e >= 0 && e + 4 <= V) {
-            x[i] = load4(in + e);
-        } else {
-            float *f = reinterpret_cast<float *>(&x[i]);
+        for (int i = 0; i < DEEP; ++i)
+            x[i] = __ldcs(src + min(g0 + i * kThreads, groups - 1));
+        if (mask) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (e + j >= 0 && e + j < V)
-                    f[j] = load1(in + e + j);
+            for (int i = 0; i < DEEP; ++i)
+                word[i] = __ldg(mask + ((head + min(g0 + i * kThreads, groups - 1) * N) >> 5));
+            if (odd) {
+#pragma unroll
+                for (int i = 0; i < DEEP; ++i)
+                    next[i] = __ldg(
+                        mask + ((head + min(g0 + i * kThreads, groups - 1) * N + N - 1) >> 5));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < DEEP; ++i) {
+            if (g0 + i * kThreads >= groups)
+                break;
+            if (mask) {
+                const int s = (head + (g0 + i * kThreads) * N) & 31;
+                const uint32_t bits = odd ? __funnelshift_r(word[i], next[i], s) : word[i] >> s;
+                uint32_t *w = reinterpret_cast<uint32_t *>(&x[i]);
+                if constexpr (N == 4) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        w[j] = bits & (1u << j) ? w[j] : 0xff800000u;
+                } else {
+                    constexpr uint32_t inf = std::is_same<IO, __half>::value ? 0xfc00u : 0xff80u;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t keep = (bits & (1u << (2 * j)) ? 0xffffu : 0u) |
+                                              (bits & (2u << (2 * j)) ? 0xffff0000u : 0u);
+                        w[j] = (w[j] & keep) | ((inf | inf << 16) & ~keep);
+                    }
+                }
+            }
+            dst[g0 + i * kThreads] = x[i];
         }
     }
-    uint32_t word[GROUPS];
+}
+
+template <typename IO, bool VEC>
+__global__ void __launch_bounds__(kThreads, 5) adjust_kernel(const __grid_constant__ LogitsArgs P)
+{
+    constexpr int N = 16 / sizeof(IO);
+    extern __shared__ __align__(16) uint32_t shared[];
+    __shared__ uint32_t warp_sum_[kThreads / 32];
+    __shared__ int twice;  // the bias list names a token twice
+    uint32_t *bitmap = shared, *before = shared + P.words;   // named tokens; those of earlier words
+    uint32_t *counts = before + P.words, *owner = counts + kPlaces, *ids = owner + kPlaces;
+    const int tid = threadIdx.x, lane = tid & 31, V = int(P.V);  // (n_vocab <= 2^26)
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t b = blockIdx.x / unsigned(P.parts);
+    const int rank = int(blockIdx.x % unsigned(P.parts));
+    const IO *in = static_cast<const IO *>(P.in) + b * P.ld_in;
+    IO *out = static_cast<IO *>(P.out) + b * P.ld_out;
     const uint32_t *mask = P.mask ? P.mask + b * P.ld_mask : nullptr;
-#pragma unroll
-    for (int i = 0; i < GROUPS; ++i) {
-        const int e = v0 + (i * kThreads + tid) * 4;
-        word[i] = mask && e < V ? __ldg(mask + (e < 0 ? 0 : e >> 5)) : 0u;
-    }
+    // parts end at 16-byte boundaries
+    const int shift = VEC ? int((reinterpret_cast<uintptr_t>(in) / sizeof(IO)) & (N - 1)) : 0;
+    const int lo = min(V, max(0, rank * P.part - shift));
+    const int hi = rank + 1 == P.parts ? V : min(V, max(0, (rank + 1) * P.part - shift));
+
     int64_t h0 = 0, h1 = 0, b0 = 0, b1 = 0;
     if (P.n_history > 0) {
         h0 = clamp64(__ldg(P.history_offsets + b), P.n_history);
@@ -87,152 +156,151 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const __grid_constant_
         b0 = clamp64(__ldg(P.bias_offsets + b), P.n_biases);
         b1 = clamp64(__ldg(P.bias_offsets + b + 1), P.n_biases);
     }
+    // the lists' first tokens are on their way while the part is streamed
+    int held[kAhead], held_bias = -1;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+        held[j] = h0 + tid + j * kThreads < h1 ? __ldg(P.history + h0 + tid + j * kThreads) : -1;
+    if (b0 + tid < b1)
+        held_bias = __ldg(P.bias_ids + b0 + tid);
+    const bool in_place = P.in == P.out;
+    if (!in_place || mask)
+        stream_part<IO, VEC>(in, out, mask, lo, hi, V);
+    if (h0 >= h1 && b0 >= b1)
+        return;  // (the row's other blocks do the same)
     const float r = P.repeat ? __ldg(P.repeat + b) : 1.f;
     const float presence = P.presence ? __ldg(P.presence + b) : 0.f;
     const float frequency = P.frequency ? __ldg(P.frequency + b) : 0.f;
-    const bool counted = h1 > h0, biased = b1 > b0;
-    if (counted || biased) {
-        // a token's place in this chunk, or -1
-        auto place = [&](int id) {
-            const unsigned at = unsigned(id) - unsigned(v0);
-            return unsigned(id) < unsigned(V) && at < unsigned(CHUNK) ? int(at) : -1;
-        };
-        // the first of the lists are on their way while the arrays are cleared
-        int id[AHEAD], bid = -1;
-        float bval = 0.f;
+
+    // f(token) for the history, f(token, entry) for the biases
+    auto each_said = [&](auto f) {
 #pragma unroll
-        for (int j = 0; j < AHEAD; ++j) {
-            const int64_t i = h0 + tid + j * kThreads;
-            id[j] = i < h1 ? __ldg(P.history + i) : -1;
-        }
-        if (b0 + tid < b1) {
-            bid = __ldg(P.bias_ids + b0 + tid);
-            bval = __ldg(P.bias_values + b0 + tid);
-        }
-#pragma unroll
-        for (int i = 0; i < GROUPS; ++i) {
-            const int at = (i * kThreads + tid) * 4;
-            if (counted)
-                *reinterpret_cast<uint4 *>(counts + at) = make_uint4(0, 0, 0, 0);
-            if (biased)
-                *reinterpret_cast<uint4 *>(bias + at) =
-                    make_uint4(kNoOwner, kNoOwner, kNoOwner, kNoOwner);
-        }
+        for (int j = 0; j < kAhead; ++j)
+            f(held[j]);
+#pragma unroll 4
+        for (int64_t i = h0 + tid + kAhead * kThreads; i < h1; i += kThreads)
+            f(__ldg(P.history + i));
+    };
+    auto each_bias = [&](auto f) {
+        f(held_bias, uint32_t(tid));
+        for (int64_t i = b0 + tid + kThreads; i < b1; i += kThreads)
+            f(__ldg(P.bias_ids + i), uint32_t(i - b0));
+    };
+    for (int w0 = lo; w0 < hi; w0 += 32 * P.words) {
+        const int span = min(hi - w0, 32 * P.words), words = (span + 31) / 32;
+        for (int i = tid; i < words; i += kThreads)
+            bitmap[i] = 0u;
+        if (tid == 0)
+            twice = 0;
         __syncthreads();
-        for (int64_t i = h0 + tid; i < h1; i += AHEAD * kThreads) {
-#pragma unroll
-            for (int j = 0; j < AHEAD; ++j) {
-                const int at = place(id[j]);
-                if (at >= 0)
-                    atomicAdd(counts + at, 1u);
-                const int64_t next = i + (AHEAD + j) * kThreads;
-                id[j] = next < h1 ? __ldg(P.history + next) : -1;
+        auto note = [&](int token) {
+            const unsigned at = unsigned(token) - unsigned(w0);
+            if (token >= 0 && at < unsigned(span))
+                atomicOr(bitmap + (at >> 5), 1u << (at & 31));
+        };
+        each_said(note);
+        each_bias([&](int token, uint32_t) { note(token); });
+        __syncthreads();
+        // ranks: a thread takes `run` consecutive words
+        const int run = (words + kThreads - 1) / kThreads;
+        uint32_t mine = 0;
+        for (int k = 0; k < run; ++k) {
+            const int i = tid * run + k;
+            if (i < words) {
+                before[i] = mine;
+                mine += __popc(bitmap[i]);
             }
         }
-        if (biased) {
-            int at = place(bid);
-            if (at >= 0)
-                atomicMin(bias + at, uint32_t(tid));
-            for (int64_t i = b0 + tid + kThreads; i < b1; i += kThreads) {
-                const int a2 = place(__ldg(P.bias_ids + i));
-                if (a2 >= 0)
-                    atomicMin(bias + a2, uint32_t(i - b0));
+        uint32_t upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
+            upto += lane >= o ? v : 0u;
+        }
+        if (lane == 31)
+            warp_sum_[tid >> 5] = upto;
+        __syncthreads();
+        uint32_t total = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            upto += w < (tid >> 5) ? warp_sum_[w] : 0u;
+            total += warp_sum_[w];
+        }
+        for (int k = 0; k < run; ++k)
+            if (tid * run + k < words)
+                before[tid * run + k] += upto - mine;
+        // named tokens by rank, kPlaces at a time
+        for (uint32_t first = 0; first < total; first += kPlaces) {
+            const uint32_t n = min(uint32_t(kPlaces), total - first);
+            for (uint32_t i = tid; i < n; i += kThreads) {
+                counts[i] = 0u;
+                owner[i] = kNoOwner;
             }
             __syncthreads();
-            bool twice = at >= 0 && bias[at] != uint32_t(tid);  // a token of this chunk named twice
-            for (int64_t i = b0 + tid + kThreads; i < b1; i += kThreads) {
-                const int a2 = place(__ldg(P.bias_ids + i));
-                twice |= a2 >= 0 && bias[a2] != uint32_t(i - b0);
-            }
-            twice = __syncthreads_or(twice);
-            for (int64_t i = b0 + tid; i < b1; i += kThreads) {
-                if (i >= b0 + kThreads) {
-                    bid = __ldg(P.bias_ids + i);
-                    bval = __ldg(P.bias_values + i);
-                    at = place(bid);
+            auto place = [&](int token) {  // its place, or kPlaces and more
+                const unsigned at = unsigned(token) - unsigned(w0);
+                if (token < 0 || at >= unsigned(span))
+                    return uint32_t(kPlaces);
+                return before[at >> 5] + __popc(bitmap[at >> 5] & ((1u << (at & 31)) - 1u)) - first;
+            };
+            each_said([&](int token) {
+                const uint32_t p = place(token);
+                if (p < kPlaces) {
+                    atomicAdd(counts + p, 1u);
+                    ids[p] = token;
                 }
-                if (at < 0)
-                    continue;
-                float sum = bval;
-                if (twice) {
-                    // (the owners' indices are being overwritten: look at the list)
-                    int64_t k = b0;
-                    while (k < i && __ldg(P.bias_ids + k) != bid)
-                        ++k;
-                    if (k < i)
-                        continue;
-                    for (k = i + 1; k < b1; ++k)
-                        if (__ldg(P.bias_ids + k) == bid)
-                            sum = __fadd_rn(sum, __ldg(P.bias_values + k));
+            });
+            each_bias([&](int token, uint32_t i) {
+                const uint32_t p = place(token);
+                if (p < kPlaces) {
+                    ids[p] = token;
+                    if (atomicMin(owner + p, i) != kNoOwner)
+                        twice = 1;
                 }
-                const uint32_t bits = __float_as_uint(sum);
-                bias[at] = bits == kNoOwner ? 0x7fffffffu : bits;
+            });
+            __syncthreads();
+            for (uint32_t p = tid; p < n; p += kThreads) {
+                const int token = int(ids[p]);
+                const uint32_t c = counts[p], first_bias = owner[p];
+                float z = load1(in + token);
+                const bool banned = mask && !(mask_bits(mask, token, V) & 1u);
+                if (c) {
+                    z = z > 0.f ? __fdiv_rn(z, r) : __fmul_rn(z, r);
+                    z = __fsub_rn(z, __fadd_rn(presence, __fmul_rn(frequency, float(c))));
+                }
+                if (first_bias != kNoOwner) {
+                    const int64_t o = b0 + first_bias;
+                    float sum = __ldg(P.bias_values + o);
+                    if (twice)
+                        for (int64_t k = o + 1; k < b1; ++k)
+                            if (__ldg(P.bias_ids + k) == token)
+                                sum = __fadd_rn(sum, __ldg(P.bias_values + k));
+                    z = __fadd_rn(z, sum);
+                }
+                store1(out + token, banned ? -INFINITY : z);
             }
-        }
-        __syncthreads();
-    }
-#pragma unroll
-    for (int i = 0; i < GROUPS; ++i) {
-        const int at = (i * kThreads + tid) * 4;
-        const int e = v0 + at;
-        if (e + 4 <= 0 || e >= V)
-            continue;
-        float *f = reinterpret_cast<float *>(&x[i]);
-        if (counted) {
-            const uint4 c4 = *reinterpret_cast<const uint4 *>(counts + at);
-            if (c4.x | c4.y | c4.z | c4.w) {
-                const uint32_t c[4] = {c4.x, c4.y, c4.z, c4.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (c[j]) {
-                        const float z = f[j] > 0.f ? __fdiv_rn(f[j], r) : __fmul_rn(f[j], r);
-                        f[j] =
-                            __fsub_rn(z, __fadd_rn(presence, __fmul_rn(frequency, float(c[j]))));
-                    }
-            }
-        }
-        if (biased) {
-            const uint4 s4 = *reinterpret_cast<const uint4 *>(bias + at);
-            if ((s4.x & s4.y & s4.z & s4.w) != kNoOwner) {
-                const uint32_t s[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (s[j] != kNoOwner)
-                        f[j] = __fadd_rn(f[j], __uint_as_float(s[j]));
-            }
-        }
-        if (mask) {
-            const int first = e < 0 ? 0 : e, w = first >> 5;
-            // (groups at odd places may reach into the next word)
-            const uint32_t hi = (first & 31) > 28 && (w + 1) * 32 < V ? __ldg(mask + w + 1) : 0u;
-            const uint32_t bits = __funnelshift_r(word[i], hi, first & 31);
-            const uint32_t four = e < 0 ? bits << -e : bits;  // bit j: logit e + j
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                f[j] = four & (1u << j) ? f[j] : -INFINITY;
-        }
-        if (VEC && e >= 0 && e + 4 <= V) {
-            store4(out + e, x[i]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (e + j >= 0 && e + j < V)
-                    store1(out + e + j, f[j]);
+            __syncthreads();
         }
     }
 }
 
-template <typename IO, int GROUPS, bool VEC>
-cudaError_t launch(const LogitsArgs &a, cudaStream_t s)
+template <typename IO, bool VEC>
+cudaError_t launch(LogitsArgs a, int sm_count, cudaStream_t s)
 {
-    constexpr int CHUNK = GROUPS * kThreads * 4;
-    const auto kern = adjust_kernel<IO, GROUPS, VEC>;
-    const size_t smem = size_t(CHUNK) * 4 * ((a.n_history > 0) + (a.n_biases > 0));
-    cudaError_t e = func_smem(reinterpret_cast<const void *>(kern), smem);
-    if (e != cudaSuccess)
-        return e;
+    constexpr int N = 16 / sizeof(IO);
+    const auto kern = adjust_kernel<IO, VEC>;
+    // Every block of a row scans its lists: parts as long as still give each SM
+    // some blocks.
+    int64_t most = kLongest;
+    while (most > 1024 && a.B * ((a.V + most - 1) / most) < 4 * sm_count)
+        most /= 2;
+    a.parts = int((a.V + most - 1) / most);
+    a.part = int((a.V + N + a.parts - 1) / a.parts + N - 1) / N * N;
+    a.words = int(std::min<int64_t>(kWords, (int64_t(a.part) + N + 31) / 32 + 1));
+    const bool named = a.n_history > 0 || a.n_biases > 0;
+    const size_t smem = named ? (size_t(a.words) * 2 + kPlaces * 3) * 4 : 0;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(a.B), unsigned((a.V + 3 + CHUNK - 1) / CHUNK));
+    cfg.gridDim = dim3(unsigned(a.B * a.parts));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -247,16 +315,10 @@ cudaError_t launch(const LogitsArgs &a, cudaStream_t s)
 template <typename IO>
 cudaError_t launch_io(const LogitsArgs &a, int sm_count, cudaStream_t s)
 {
-    const size_t unit = 4 * sizeof(IO);
     const bool vec =
-        (reinterpret_cast<uintptr_t>(a.in) - reinterpret_cast<uintptr_t>(a.out)) % unit == 0 &&
-        (a.B == 1 || size_t(a.ld_in - a.ld_out) * sizeof(IO) % unit == 0);
-    // Long chunks share a row's history scan; short ones spread a small batch
-    // over the SMs.
-    const bool wide = a.B * a.V >= int64_t(sm_count) * 4 * 8192;
-    if (wide)
-        return vec ? launch<IO, WIDE, true>(a, s) : launch<IO, WIDE, false>(a, s);
-    return vec ? launch<IO, 2, true>(a, s) : launch<IO, 2, false>(a, s);
+        (reinterpret_cast<uintptr_t>(a.in) - reinterpret_cast<uintptr_t>(a.out)) % 16 == 0 &&
+        (a.B == 1 || uint64_t(a.ld_in - a.ld_out) * sizeof(IO) % 16 == 0);
+    return vec ? launch<IO, true>(a, sm_count, s) : launch<IO, false>(a, sm_count, s);
 }
 
 } // namespace

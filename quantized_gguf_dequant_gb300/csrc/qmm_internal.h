@@ -500,6 +500,8 @@ struct LogitsArgs {
     int64_t n_biases;
     const uint32_t *mask;
     int64_t ld_mask;
+    // set by the launcher: blocks of a row, logits of a block, bitmap words
+    int parts, part, words;
 };
 cudaError_t launch_logits_adjust(const LogitsArgs &a, int sm_count, cudaStream_t s);
 
