@@ -56,16 +56,20 @@ namespace qmm {
 
 namespace {
 
+#ifndef ATTN_TWO
+#define ATTN_TWO 64
+#define ATTN_Q8_TWO 128
+#endif
 #ifndef ATTN_W
 #define ATTN_W 4
 #endif
-constexpr int kTile = 16;  // keys per tile (the instruction's k and two n)
+constexpr int kGroup = 16;  // keys of an instruction group (the instruction's k and two n)
 constexpr int kLens = 512;  // lengths kept in shared memory
 // The fixed part of an item's time in a block (its first loads, its joins), in
-// the time of 16-key tiles; blocks get equal shares of tiles and these.
+// the time of 16-key groups; blocks get equal shares of groups and these.
 constexpr int kItemCost = 12;
 // A block takes at least so much: splitting an item costs a join, which is
-// worth it from about twenty saved tiles on.
+// worth it from about twenty saved groups on.
 constexpr int kMinUnits = 36;
 constexpr int kStatic = 2560;  // the kernel's static shared memory, at most
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -74,20 +78,34 @@ enum Kind { kF16, kBF16, kQ8 };
 
 // Warps of a block.
 constexpr int attn_warps(Kind, int) { return ATTN_W; }
+// Groups of a tile, the keys a warp takes in one step.  Two share the step's
+// fixed instructions and its latency where shared memory still holds enough
+// warps' stages.
+constexpr int attn_groups(Kind k, int D) { return k == kQ8 ? (D <= ATTN_Q8_TWO ? 2 : 1) : (D <= ATTN_TWO ? 2 : 1); }
 
 template <Kind KIND, int D, int NH>
 struct Shape {
     static constexpr int W = attn_warps(KIND, D), THREADS = 32 * W;
+    static constexpr int KT = attn_groups(KIND, D), TILE = KT * kGroup;
+    static constexpr unsigned ALL = KT == 2 ? 0xffffffffu : 0xffffu;  // every key valid
+    static constexpr int COST = kItemCost / KT, MIN_UNITS = kMinUnits / KT;  // in tiles
     static constexpr int ROWB = KIND == kQ8 ? D : 2 * D;           // bytes of a row
-    // Rows in shared memory: 16-byte chunk c of row r sits at c ^ (r & 7) where
-    // rows are whole 128 bytes, else rows are padded by 16 bytes; either way the
-    // eight rows of an ldmatrix lie in different banks.  Q8_0 rows of 32 or 96
-    // mod 128 bytes spread its 8-byte loads.
-    static constexpr bool SWZ = KIND != kQ8 && D % 64 == 0;
-    static constexpr int RS = KIND == kQ8 ? ROWB + (D % 64 == 0 ? 32 : 0) : ROWB + (SWZ ? 0 : 16);
+    // Rows in shared memory.  16-bit values: 16-byte chunk c of row r sits at
+    // c ^ (r & 7), so that the eight rows of an ldmatrix lie in different banks.
+    // Q8_0: 32-byte block c sits at c ^ swz8(r), which spreads both the eight
+    // rows of its key loads and the four even or odd ones of its value loads.
+    // Rows that are not whole 128 bytes are padded instead.
+    static constexpr bool SWZ = ROWB % 128 == 0;
+    static constexpr int RS = SWZ ? ROWB : KIND == kQ8 ? ROWB + (D % 64 == 0 ? 32 : 0) : ROWB + 16;
+    static __host__ __device__ constexpr int swz8(int r) { return ((r & 7) ^ ((r & 7) >> 2)) & 3; }
+    // Byte of chunk ch of row r of a tile.
+    static __host__ __device__ constexpr uint32_t chunk_place(int r, int ch)
+    {
+        return r * RS + (!SWZ ? ch : KIND == kQ8 ? ch ^ (swz8(r) * 2) : ch ^ (r & 7)) * 16;
+    }
     static constexpr int SP = kv_scales_per_row(D);
     static constexpr int SCB = KIND == kQ8 ? SP * 2 : 0;           // bytes of a row's scales
-    static constexpr int STAGE = 2 * kTile * (RS + SCB);
+    static constexpr int STAGE = 2 * TILE * (RS + SCB);
     static constexpr int CHUNKS = ROWB / 16;                       // 16-byte chunks of a row
     static constexpr int KSTEPS = D / 16;
     // q's operand registers in shared memory: four a lane (two pieces of eight
@@ -112,23 +130,22 @@ struct Shape {
     static constexpr bool POW2 = 32 % CHUNKS == 0;
     static __device__ __forceinline__ uint32_t copy_base(int lane)
     {
-        const int r = lane / CHUNKS, ch = lane % CHUNKS;
-        return r * RS + (SWZ ? ch ^ r : ch) * 16;
+        return chunk_place(lane / CHUNKS, lane % CHUNKS);
     }
     static __device__ __forceinline__ uint32_t copy_at(uint32_t base, int it, int lane)
     {
-        if constexpr (POW2) {
+        if constexpr (POW2) {  // (the swizzles are linear in the row's bits)
             constexpr int R = 32 / CHUNKS;  // rows of an instruction
-            return (SWZ ? base ^ ((it * R & 7) * 16) : base) + it * R * RS;
+            return (base ^ (chunk_place(it * R, 0) - it * R * RS)) + it * R * RS;
         } else {
-            const int idx = it * 32 + lane, r = idx / CHUNKS, ch = idx % CHUNKS;
-            return r * RS + (SWZ ? ch ^ (r & 7) : ch) * 16;
+            const int idx = it * 32 + lane;
+            return chunk_place(idx / CHUNKS, idx % CHUNKS);
         }
     }
-    // Address of 16-value column ks of a row, from that of column 0.
-    static __device__ __forceinline__ uint32_t chunk_at(uint32_t row, int ks)
+    // Address of 32-byte column c of a row, from that of column 0.
+    static __device__ __forceinline__ uint32_t column(uint32_t row, int c)
     {
-        return SWZ ? (row ^ ((ks & 3) * 32)) + (ks >> 2) * 128 : row + ks * 32;
+        return SWZ ? (row ^ ((c & 3) * 32)) + (c >> 2) * 128 : row + c * 32;
     }
 };
 
@@ -243,18 +260,19 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t biased, unsigned sel)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// The tile list of one sequence: keys [lo, hi), tiles t0 .. t0 + n - 1 (in
-// units of 16 keys from key 0).
+// The tile list of one sequence: keys [lo, hi), tiles t0 .. t0 + n - 1 (tiles
+// counted from key 0).
 struct Span {
     int lo, hi, t0, n;
 };
-__device__ __forceinline__ Span span_of(const AttnArgs &a, int len)
+template <int TILE>
+__device__ __forceinline__ Span tiles_of(const AttnArgs &a, int len)
 {
     Span s;
     s.hi = max(0, min(len, int(min(a.ld_table * a.c.page_size, int64_t(0x7fffffe0)))));
     s.lo = a.window > 0 ? max(0, s.hi - a.window) : 0;
-    s.t0 = s.lo / kTile;
-    s.n = s.hi > s.lo ? (s.hi + kTile - 1) / kTile - s.t0 : 0;
+    s.t0 = s.lo / TILE;
+    s.n = s.hi > s.lo ? (s.hi + TILE - 1) / TILE - s.t0 : 0;
     return s;
 }
 
@@ -310,7 +328,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
     attn_kernel(const __grid_constant__ AttnParams P)
 {
     using S = Shape<KIND, D, NH>;
-    constexpr int kWarps = S::W, kThreads = S::THREADS;
+    constexpr int kWarps = S::W, kThreads = S::THREADS, KT = S::KT, TILE = S::TILE;
     using H = Half<KIND>;
     constexpr int STAGES = S::STAGES;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -333,12 +351,12 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
     pdl_launch_dependents();
 
     // ---- the plan: prefix sums of the sequences' units
-    auto units_of = [&](int n) { return n ? int64_t(n + kItemCost) * P.items : int64_t(0); };
+    auto units_of = [&](int n) { return n ? int64_t(n + S::COST) * P.items : int64_t(0); };
     auto len_of = [&](int b) { return b < kLens ? lens[b] : __ldg(A.lens + b); };
     // Sequences without keys are no one's item: their outputs are zero.
     auto fill_empty = [&]() {
         for (int b = blockIdx.x; b < A.n_seqs; b += gridDim.x) {
-            if (span_of(A, __ldg(A.lens + b)).n > 0)
+            if (tiles_of<TILE>(A, __ldg(A.lens + b)).n > 0)
                 continue;
             for (int i = tid; i < A.n_q * D / 4; i += kThreads)
                 store4_any(A.out, b * A.ldo + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f), A.dtype);
@@ -351,8 +369,8 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
     // Equal shares for all resident blocks, but no smaller ones than pay for
     // a join; those small ones divide the longest item evenly.
     auto share = [&](int64_t total, int longest) {
-        const unsigned item = unsigned(longest + kItemCost);
-        const unsigned parts = max(1u, item / unsigned(P.min_units));
+        const unsigned item = unsigned(longest + S::COST);
+        const unsigned parts = max(1u, item / unsigned(S::MIN_UNITS));
         const int64_t even = total <= 0xffffffffll
                                  ? int64_t((unsigned(total) - 1) / gridDim.x + 1)
                                  : (total - 1) / int64_t(gridDim.x) + 1;
@@ -363,7 +381,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
     if (A.n_seqs <= 32) {
         // every warp by itself, a sequence a lane
         const int len = lane < A.n_seqs ? __ldg(A.lens + lane) : 0;
-        const Span sp = span_of(A, len);
+        const Span sp = tiles_of<TILE>(A, len);
         if (blockIdx.x == 0 && warp == 0 && (len < 0 || len > sp.hi))
             atomicOr(A.status, kStatusBadLengthBit);
         if (warp == 0)
@@ -400,7 +418,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
         int most = 0;
         for (int b = sb0; b < sb1; ++b) {
             const int len = len_of(b);
-            const Span sp = span_of(A, len);
+            const Span sp = tiles_of<TILE>(A, len);
             mine += units_of(sp.n);
             most = max(most, sp.n);
             if (blockIdx.x == 0 && (len < 0 || len > sp.hi))
@@ -438,7 +456,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
         if (r0 < upto && r0 >= upto - mine) {
             int64_t at = upto - mine;
             for (int b = sb0; b < sb1; ++b) {
-                const int64_t n = units_of(span_of(A, len_of(b)).n);
+                const int64_t n = units_of(tiles_of<TILE>(A, len_of(b)).n);
                 if (r0 < at + n) {
                     found_seq = b;
                     found_at = at;
@@ -453,15 +471,20 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
         seq_len = len_of(seq);
     }
     const int64_t blk = blockIdx.x, r1 = min(total, r0 + per);
-    Span sp = span_of(A, seq_len);
+    Span sp = tiles_of<TILE>(A, seq_len);
 
     const uint32_t smem_base = smem_u32(smem);
     // this lane's row and half-chunk of an ldmatrix over 16 keys x 16 values
     const uint32_t frag_row =
-        ((lane >> 4) * 8 + (lane & 7)) * S::RS +
-        (S::SWZ ? ((lane >> 3) & 1) ^ (lane & 7) : (lane >> 3) & 1) * 16;
+        S::chunk_place((lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1);
+    // Q8_0: this lane's key row g and value rows 2t, 2t + 1 in a group
+    const uint32_t key_row = g * S::RS + (S::SWZ ? S::swz8(g) * 32 : 0) + t * 8;
+    uint32_t val_row[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+        val_row[x] = (2 * t + x) * S::RS + (S::SWZ ? S::swz8(2 * t + x) * 32 : 0) + 4 * g;
     const uint32_t copy_row = S::copy_base(lane);
-    const bool whole_tiles = C.page.d % kTile == 0;  // a tile lies in one page
+    const bool whole_groups = C.page.d % kGroup == 0;  // a group lies in one page
     const uint32_t ring = smem_base + S::QFRAG + warp * STAGES * S::STAGE;
     float *join = reinterpret_cast<float *>(smem + S::QFRAG);
     float *join_ml = join + kWarps * NH * S::OSTRIDE;
@@ -470,11 +493,11 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
         while (at >= seq_at + units_of(sp.n)) {
             seq_at += units_of(sp.n);
             ++seq;
-            sp = span_of(A, len_of(seq));
+            sp = tiles_of<TILE>(A, len_of(seq));
         }
         // the item and this block's tiles [ta, tb) of it
-        const int item = int(uint64_t(at - seq_at) / unsigned(sp.n + kItemCost));
-        const int64_t tiles_at = seq_at + int64_t(item) * (sp.n + kItemCost) + kItemCost;
+        const int item = int(uint64_t(at - seq_at) / unsigned(sp.n + S::COST));
+        const int64_t tiles_at = seq_at + int64_t(item) * (sp.n + S::COST) + S::COST;
         const int ta = int(max(int64_t(0), at - tiles_at));
         const int tb = int(max(int64_t(0), min(r1 - tiles_at, int64_t(sp.n))));
         at = tiles_at + sp.n;
@@ -487,7 +510,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
         const int32_t *table = A.table + int64_t(seq) * A.ld_table;
 
         // ---- loading
-        auto key_of = [&](int i) { return (sp.t0 + ta + warp + i * kWarps) * kTile + (lane & 15); };
+        auto key_of = [&](int i) { return (sp.t0 + ta + warp + i * kWarps) * TILE + (lane & (TILE - 1)); };
         // the page of this lane's key of tile i (a guarded load and no branch,
         // so that several are under way at once)
         auto page_id = [&](int i) -> int {
@@ -506,31 +529,36 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
             return unsigned(id) < C.n_pages;
         };
         auto issue = [&](int i, int id) {
-            const int first = (sp.t0 + ta + warp + i * kWarps) * kTile;
-            if (i < nw && whole_tiles && first >= sp.lo && first + kTile <= sp.hi &&
-                unsigned(id) < C.n_pages) {
-                // sixteen keys of one page: contiguous rows
-                const int st = i % STAGES;
+            const int first = (sp.t0 + ta + warp + i * kWarps) * TILE;
+            const int st = i % STAGES;
+            const uint32_t kdst = ring + st * S::STAGE, vdst = kdst + TILE * S::RS;
+            if (i < nw && whole_groups && first >= sp.lo && first + TILE <= sp.hi &&
+                __all_sync(0xffffffffu, unsigned(id) < C.n_pages)) {
+                // sixteen keys of one page at a time: contiguous rows
                 if (lane == 0)
-                    valid_ring[warp][st] = 0xffffu;
-                const uint32_t kdst = ring + st * S::STAGE, vdst = kdst + kTile * S::RS;
-                const uint32_t row =
-                    (uint32_t(id) * unsigned(C.n_heads) + unsigned(kvh)) * C.page.d +
-                    unsigned(first) - fast_div(C.page, unsigned(first)) * C.page.d;
-                const uint64_t o = uint64_t(row) * S::ROWB + lane * 16;
-                const uint8_t *ksrc = C.k + o, *vsrc = C.v + o;
+                    valid_ring[warp][st] = S::ALL;
 #pragma unroll
-                for (int it = 0; it < kTile * S::CHUNKS / 32; ++it) {
-                    const uint32_t at = S::copy_at(copy_row, it, lane);
-                    cp16(kdst + at, ksrc + it * 512);
-                    cp16(vdst + at, vsrc + it * 512);
-                }
-                if constexpr (KIND == kQ8) {  // SCB chunks of scales, lanes 0.. keys', 16.. values'
-                    const uint8_t *ssrc = static_cast<const uint8_t *>(lane < 16 ? C.ks : C.vs);
-                    if ((lane & 15) < S::SCB)
-                        cp16(kdst + 2 * kTile * S::RS + (lane >> 4) * kTile * S::SCB +
-                                 (lane & 15) * 16,
-                             ssrc + uint64_t(row) * S::SCB + (lane & 15) * 16);
+                for (int u = 0; u < KT; ++u) {
+                    const unsigned key = unsigned(first + u * kGroup);
+                    const unsigned pg = unsigned(KT == 1 ? id : __shfl_sync(0xffffffffu, id, u * 16));
+                    const uint32_t row = (pg * unsigned(C.n_heads) + unsigned(kvh)) * C.page.d + key -
+                                         fast_div(C.page, key) * C.page.d;
+                    const uint64_t o = uint64_t(row) * S::ROWB + lane * 16;
+                    const uint8_t *ksrc = C.k + o, *vsrc = C.v + o;
+#pragma unroll
+                    for (int it = 0; it < kGroup * S::CHUNKS / 32; ++it) {
+                        const uint32_t at = S::copy_at(copy_row, it, lane) + u * kGroup * S::RS;
+                        cp16(kdst + at, ksrc + it * 512);
+                        cp16(vdst + at, vsrc + it * 512);
+                    }
+                    if constexpr (KIND == kQ8) {
+                        // SCB chunks of scales, lanes 0.. the keys', 16.. the values'
+                        const uint8_t *ssrc = static_cast<const uint8_t *>(lane < 16 ? C.ks : C.vs);
+                        if ((lane & 15) < S::SCB)
+                            cp16(kdst + 2 * TILE * S::RS +
+                                     ((lane >> 4) * TILE + u * kGroup) * S::SCB + (lane & 15) * 16,
+                                 ssrc + uint64_t(row) * S::SCB + (lane & 15) * 16);
+                    }
                 }
             } else if (i < nw) {
                 const int j = key_of(i);
@@ -542,35 +570,33 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
                     const uint32_t off = unsigned(j) - fast_div(C.page, unsigned(j)) * C.page.d;
                     row = (uint32_t(id) * unsigned(C.n_heads) + unsigned(kvh)) * C.page.d + off;
                 }
-                const unsigned valid = __ballot_sync(0xffffffffu, ok) & 0xffffu;
-                const int st = i % STAGES;
+                const unsigned valid = __ballot_sync(0xffffffffu, ok) & S::ALL;
                 if (lane == 0)
                     valid_ring[warp][st] = valid;
-                const uint32_t kdst = ring + st * S::STAGE, vdst = kdst + kTile * S::RS;
 #pragma unroll
-                for (int it = 0; it < kTile * S::CHUNKS / 32; ++it) {
+                for (int it = 0; it < TILE * S::CHUNKS / 32; ++it) {
                     const int idx = it * 32 + lane;
                     const int r = idx / S::CHUNKS, ch = idx % S::CHUNKS;
                     const uint64_t o =
                         uint64_t(__shfl_sync(0xffffffffu, row, r)) * S::ROWB + ch * 16;
                     const unsigned bytes = (valid >> r) & 1u ? 16u : 0u;
-                    const unsigned at = r * S::RS + (S::SWZ ? ch ^ (r & 7) : ch) * 16;
+                    const uint32_t at = S::chunk_place(r, ch);
                     cp16(kdst + at, C.k + o, bytes);
                     cp16(vdst + at, C.v + o, bytes);
                 }
                 if constexpr (KIND == kQ8) {
                     constexpr int W = S::SCB / 4;  // words of a row's scales
-                    const uint32_t sdst = kdst + 2 * kTile * S::RS;
+                    const uint32_t sdst = kdst + 2 * TILE * S::RS;
 #pragma unroll
-                    for (int it = 0; it < (kTile * W + 31) / 32; ++it) {
+                    for (int it = 0; it < (TILE * W + 31) / 32; ++it) {
                         const int idx = it * 32 + lane;
-                        const int r = (idx / W) & 15, w = idx % W;
+                        const int r = (idx / W) & (TILE - 1), w = idx % W;
                         const uint64_t o =
                             uint64_t(__shfl_sync(0xffffffffu, row, r)) * S::SCB + w * 4;
                         const unsigned bytes = (valid >> r) & 1u ? 4u : 0u;
-                        if (idx < kTile * W) {
+                        if (idx < TILE * W) {
                             cp4(sdst + idx * 4, static_cast<const uint8_t *>(C.ks) + o, bytes);
-                            cp4(sdst + kTile * S::SCB + idx * 4,
+                            cp4(sdst + TILE * S::SCB + idx * 4,
                                 static_cast<const uint8_t *>(C.vs) + o, bytes);
                         }
                     }
@@ -706,146 +732,171 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
         int vexp = -126;               // Q8_0: exponent of the largest value scale so far
         float O[D / 16][4] = {};
 
+        auto key_in = [&](int x) { return 2 * t + (x & 1) + (x >> 1) * 8; };  // of a group
         for (int i = 0; i < nw; ++i) {
             issue(i + STAGES - 1, next_id);
             next_id = page_id(i + STAGES);
             cp_wait<STAGES - 1>();
             __syncwarp();
             const int st = i % STAGES;
-            const uint32_t kb = ring + st * S::STAGE, vb = kb + kTile * S::RS;
-            const uint32_t ksb = vb + kTile * S::RS, vsb = ksb + kTile * S::SCB;
+            const uint32_t kb = ring + st * S::STAGE, vb = kb + TILE * S::RS;
+            const uint32_t ksb = vb + TILE * S::RS, vsb = ksb + TILE * S::SCB;
 
-            // ---- scores of head hd at keys 2t, 2t+1, 2t+8, 2t+9
-            float s[4];
+            // ---- scores of head hd at keys 2t, 2t+1, 2t+8, 2t+9 of each group
+            float s[KT][4];
             if constexpr (KIND == kQ8) {
-                s[0] = s[1] = s[2] = s[3] = 0.f;
-                uint32_t ksc[4][S::SP / 2];
+                uint32_t ksc[KT][4][S::SP / 2];
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    lds_words(ksc[x], ksb + (2 * t + (x & 1) + (x >> 1) * 8) * S::SCB);
+                for (int u = 0; u < KT; ++u)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        s[u][x] = 0.f;
+                        lds_words(ksc[u][x], ksb + (u * kGroup + key_in(x)) * S::SCB);
+                    }
 #pragma unroll
                 for (int blk = 0; blk < D / 32; ++blk) {
                     // codes + 128 as subnormals; the 128s' part of the sum, which
                     // is q's, is where it starts from
                     uint4 a[2];
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const uint8_t *fr = smem + ((2 * blk + u) * 32 + lane) * 16;
+                    for (int h = 0; h < 2; ++h) {
+                        const uint8_t *fr = smem + ((2 * blk + h) * 32 + lane) * 16;
                         if constexpr (NH == 8) {
-                            a[u] = *reinterpret_cast<const uint4 *>(fr);
+                            a[h] = *reinterpret_cast<const uint4 *>(fr);
                         } else {  // rows 8-15 are empty
-                            a[u].x = *reinterpret_cast<const uint32_t *>(fr);
-                            a[u].y = 0u;
-                            a[u].z = *reinterpret_cast<const uint32_t *>(fr + 8);
-                            a[u].w = 0u;
+                            a[h].x = *reinterpret_cast<const uint32_t *>(fr);
+                            a[h].y = 0u;
+                            a[h].z = *reinterpret_cast<const uint32_t *>(fr + 8);
+                            a[h].w = 0u;
                         }
                     }
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        float c[4] = {qoff[blk], qoff[blk], 0.f, 0.f};
-                        uint2 w = lds64(kb + (g + n * 8) * S::RS + blk * 32 + t * 8);
-                        w.x ^= 0x80808080u;
-                        w.y ^= 0x80808080u;
-                        mma<KIND>(c, a[0].x, a[0].y, a[0].z, a[0].w, bytes_f16(w.x, 0x4140),
-                                  bytes_f16(w.x, 0x4342));
-                        mma<KIND>(c, a[1].x, a[1].y, a[1].z, a[1].w, bytes_f16(w.y, 0x4140),
-                                  bytes_f16(w.y, 0x4342));
+                    for (int u = 0; u < KT; ++u)
 #pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const float2 sc = unpack2(ksc[2 * n + y][blk / 2], __half());
-                            s[2 * n + y] += (NH == 8 ? c[y] + c[2 + y] : c[y]) *
-                                            (blk & 1 ? sc.y : sc.x);
+                        for (int n = 0; n < 2; ++n) {
+                            float c[4] = {qoff[blk], qoff[blk], 0.f, 0.f};
+                            uint2 w = lds64(
+                                S::column(kb + (u * kGroup + n * 8) * S::RS + key_row, blk));
+                            w.x ^= 0x80808080u;
+                            w.y ^= 0x80808080u;
+                            mma<KIND>(c, a[0].x, a[0].y, a[0].z, a[0].w, bytes_f16(w.x, 0x4140),
+                                      bytes_f16(w.x, 0x4342));
+                            mma<KIND>(c, a[1].x, a[1].y, a[1].z, a[1].w, bytes_f16(w.y, 0x4140),
+                                      bytes_f16(w.y, 0x4342));
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const float2 sc = unpack2(ksc[u][2 * n + y][blk / 2], __half());
+                                s[u][2 * n + y] += (NH == 8 ? c[y] + c[2 + y] : c[y]) *
+                                                   (blk & 1 ? sc.y : sc.x);
+                            }
                         }
-                    }
                 }
             } else {
                 // two chains of sums a key block, for the instructions' latency
-                float c[2][2][4] = {}, third[2][4] = {};
-                const uint32_t kaddr = kb + frag_row;
+                float c[KT][2][2][4] = {}, third[KT][2][4] = {};
 #pragma unroll
                 for (int ks = 0; ks < S::KSTEPS; ++ks) {
-                    uint32_t b[4];
-                    ldsm4(b, S::chunk_at(kaddr, ks));
                     const uint4 a =
                         *reinterpret_cast<const uint4 *>(smem + (ks * 32 + lane) * 16);
-                    mma<KIND>(c[ks & 1][0], a.x, a.y, a.z, a.w, b[0], b[1]);
-                    mma<KIND>(c[ks & 1][1], a.x, a.y, a.z, a.w, b[2], b[3]);
-                    if constexpr (S::THIRD) {
-                        const uint2 a3 = *reinterpret_cast<const uint2 *>(
-                            smem + S::KSTEPS * 512 + (ks * 32 + lane) * 8);
-                        mma<KIND>(third[0], a3.x, 0u, a3.y, 0u, b[0], b[1]);
-                        mma<KIND>(third[1], a3.x, 0u, a3.y, 0u, b[2], b[3]);
+                    uint2 a3 = make_uint2(0u, 0u);
+                    if constexpr (S::THIRD)
+                        a3 = *reinterpret_cast<const uint2 *>(smem + S::KSTEPS * 512 +
+                                                              (ks * 32 + lane) * 8);
+#pragma unroll
+                    for (int u = 0; u < KT; ++u) {
+                        uint32_t b[4];
+                        ldsm4(b, S::column(kb + u * kGroup * S::RS + frag_row, ks));
+                        mma<KIND>(c[u][ks & 1][0], a.x, a.y, a.z, a.w, b[0], b[1]);
+                        mma<KIND>(c[u][ks & 1][1], a.x, a.y, a.z, a.w, b[2], b[3]);
+                        if constexpr (S::THIRD) {
+                            mma<KIND>(third[u][0], a3.x, 0u, a3.y, 0u, b[0], b[1]);
+                            mma<KIND>(third[u][1], a3.x, 0u, a3.y, 0u, b[2], b[3]);
+                        }
                     }
                 }
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int n = x >> 1, y = x & 1;
-                    // the smaller pieces first
-                    float v = c[0][n][y + 2] + c[1][n][y + 2];
-                    if constexpr (S::THIRD)
-                        v += third[n][y];
-                    s[x] = v + (c[0][n][y] + c[1][n][y]);
-                }
-            }
-            if constexpr (NH == 4) {  // the other pieces' rows
+                for (int u = 0; u < KT; ++u)
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    s[x] += __shfl_xor_sync(0xffffffffu, s[x], 16);
+                    for (int x = 0; x < 4; ++x) {
+                        const int n = x >> 1, y = x & 1;
+                        // the smaller pieces first
+                        float v = c[u][0][n][y + 2] + c[u][1][n][y + 2];
+                        if constexpr (S::THIRD)
+                            v += third[u][n][y];
+                        s[u][x] = v + (c[u][0][n][y] + c[u][1][n][y]);
+                    }
             }
+            float check = 0.f;
+#pragma unroll
+            for (int u = 0; u < KT; ++u)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    if constexpr (NH == 4)  // the other pieces' rows
+                        s[u][x] += __shfl_xor_sync(0xffffffffu, s[u][x], 16);
+                    check += s[u][x] * 0.f;
+                }
             const unsigned valid = valid_ring[warp][st];
-            const int key0 = (sp.t0 + ta + warp + i * kWarps) * kTile;
+            const int key0 = (sp.t0 + ta + warp + i * kWarps) * TILE;
             // An infinite key component times pieces of q gives NaN where the
             // product with q itself is infinite: settle it with q itself.
-            const bool odd = qfinite[hd] && !(s[0] + s[1] + s[2] + s[3] == s[0] + s[1] + s[2] + s[3]);
-            if (__any_sync(0xffffffffu, odd)) {
+            if (__any_sync(0xffffffffu, check != 0.f && qfinite[hd])) {
                 const int64_t q0 = int64_t(seq) * A.ldq + int64_t(head0 + hd) * D;
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    uint32_t row;
-                    if (!qfinite[hd] || hd >= nh || s[x] == s[x] ||
-                        !row_of(key0 + 2 * t + (x & 1) + (x >> 1) * 8, row))
-                        continue;
-                    float dot = 0.f;
-                    for (int d = 0; d < D; ++d)
-                        dot += load_any(A.q, q0 + d, A.dtype) *
-                               value_at<KIND, D>(C.k, C.ks, row, d);
-                    s[x] = dot * exp2i(qexp[hd]) * (KIND == kQ8 ? 0x1p-24f : 1.f);
-                }
+                for (int u = 0; u < KT; ++u)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        uint32_t row;
+                        if (!qfinite[hd] || hd >= nh || s[u][x] == s[u][x] ||
+                            !row_of(key0 + u * kGroup + key_in(x), row))
+                            continue;
+                        float dot = 0.f;
+#pragma unroll 1
+                        for (int d = 0; d < D; ++d)
+                            dot += load_any(A.q, q0 + d, A.dtype) *
+                                   value_at<KIND, D>(C.k, C.ks, row, d);
+                        s[u][x] = dot * exp2i(qexp[hd]) * (KIND == kQ8 ? 0x1p-24f : 1.f);
+                    }
             }
             // scores in base 2
-            if (A.softcap > 0.f) {
+            float tmax = -INFINITY;
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    s[x] = A.softcap * kLog2e * tanhf(s[x] * qscale * cap_inv);
-            } else {
+            for (int u = 0; u < KT; ++u) {
+                if (A.softcap > 0.f) {
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    s[x] *= qscale * kLog2e;
+                    for (int x = 0; x < 4; ++x)
+                        s[u][x] = A.softcap * kLog2e * tanhf(s[u][x] * qscale * cap_inv);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        s[u][x] *= qscale * kLog2e;
+                }
+                if (A.alibi) {
+                    const float back = float(key0 + u * kGroup + 2 * t - (sp.hi - 1));
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        s[u][x] += slope * (back + float((x & 1) + (x >> 1) * 8));
+                }
+                if (valid != S::ALL) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        s[u][x] = (valid >> (u * kGroup + key_in(x))) & 1u ? s[u][x] : -INFINITY;
+                }
+                tmax = fmaxf(tmax, fmaxf(fmaxf(s[u][0], s[u][1]), fmaxf(s[u][2], s[u][3])));
             }
-            if (A.alibi) {
-                const float back = float(key0 + 2 * t - (sp.hi - 1));
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    s[x] += slope * (back + float((x & 1) + (x >> 1) * 8));
-            }
-            if (valid != 0xffffu) {
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    s[x] = (valid >> (2 * t + (x & 1) + (x >> 1) * 8)) & 1u ? s[x] : -INFINITY;
-            }
-            float tmax = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
             tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 1));
             tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 2));
             const float mn = fmaxf(m, tmax);
             const float base = mn == -INFINITY ? 0.f : mn;
             const float corr = ex2(m - base);  // 0 while nothing was seen
             m = mn;
-            float p[4], psum = 0.f;
+            float p[KT][4], psum = 0.f;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                p[x] = ex2(s[x] - (base - kBias));
-                psum += p[x];
-            }
+            for (int u = 0; u < KT; ++u)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    p[u][x] = ex2(s[u][x] - (base - kBias));
+                    psum += p[u][x];
+                }
             l = l * corr + psum;
             // O's columns 2t and 2t+1 are heads (and with four heads, pieces)
             float f0 = __shfl_sync(0xffffffffu, corr, 8 * t),
@@ -855,16 +906,19 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
             if constexpr (KIND == kQ8) {
                 // the largest value scale of the tile moves the common exponent up
                 __half2 mx = __half2half2(__ushort_as_half(0));
-                uint32_t vsc[4][S::SP / 2];
+                uint32_t vsc[KT][4][S::SP / 2];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    lds_words(vsc[x], vsb + (2 * t + (x & 1) + (x >> 1) * 8) * S::SCB);
-                    if (D % 64 != 0)
-                        vsc[x][S::SP / 2 - 1] &= 0xffffu;  // the odd half is padding
+                for (int u = 0; u < KT; ++u)
 #pragma unroll
-                    for (int w = 0; w < S::SP / 2; ++w)
-                        mx = __hmax2(mx, __habs2(*reinterpret_cast<const __half2 *>(&vsc[x][w])));
-                }
+                    for (int x = 0; x < 4; ++x) {
+                        lds_words(vsc[u][x], vsb + (u * kGroup + key_in(x)) * S::SCB);
+                        if (D % 64 != 0)
+                            vsc[u][x][S::SP / 2 - 1] &= 0xffffu;  // the odd half is padding
+#pragma unroll
+                        for (int w = 0; w < S::SP / 2; ++w)
+                            mx = __hmax2(
+                                mx, __habs2(*reinterpret_cast<const __half2 *>(&vsc[u][x][w])));
+                    }
                 float dm = __half2float(__hmax(__low2half(mx), __high2half(mx)));
                 dm = fmaxf(dm, __shfl_xor_sync(0xffffffffu, dm, 1));
                 dm = fmaxf(dm, __shfl_xor_sync(0xffffffffu, dm, 2));
@@ -877,78 +931,90 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
                 vexp = ve;
                 const float up = exp2i(min(126, 14 - ve));
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    p[x] *= up;
-#pragma unroll
-                for (int blk = 0; blk < D / 32; ++blk) {
-                    uint32_t bp[2][2];
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const float2 s0 = unpack2(vsc[2 * n][blk / 2], __half());
-                        const float2 s1 = unpack2(vsc[2 * n + 1][blk / 2], __half());
-                        const float u0 = p[2 * n] * (blk & 1 ? s0.y : s0.x);
-                        const float u1 = p[2 * n + 1] * (blk & 1 ? s1.y : s1.x);
-                        bp[0][n] = pack2(u0, u1, H());
-                        const float2 hf = unpack2(bp[0][n], H());
-                        bp[1][n] = pack2(u0 - hf.x, u1 - hf.y, H());
-                        if constexpr (NH == 4)  // columns 4-7 carry the second piece
-                            bp[0][n] = g < 4 ? bp[0][n] : bp[1][n];
-                    }
-                    uint32_t w[4];
+                for (int u = 0; u < KT; ++u)
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
-                        w[x] = lds32(vb + (2 * t + (x & 1) + (x >> 1) * 8) * S::RS + blk * 32 +
-                                     4 * g) ^ 0x80808080u;
-                    const uint32_t e01 = __byte_perm(w[0], w[1], 0x5140),
-                                   e23 = __byte_perm(w[0], w[1], 0x7362),
-                                   o01 = __byte_perm(w[2], w[3], 0x5140),
-                                   o23 = __byte_perm(w[2], w[3], 0x7362);
+                        p[u][x] *= up;
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const uint32_t a0 = codes_f16(u ? e23 : e01, 0x4140);
-                        const uint32_t a1 = codes_f16(u ? e23 : e01, 0x4342);
-                        const uint32_t a2 = codes_f16(u ? o23 : o01, 0x4140);
-                        const uint32_t a3 = codes_f16(u ? o23 : o01, 0x4342);
-                        float c[4] = {};
-                        if constexpr (NH == 8)
-                            mma<KIND>(c, a0, a1, a2, a3, bp[1][0], bp[1][1]);
-                        mma<KIND>(c, a0, a1, a2, a3, bp[0][0], bp[0][1]);
-                        float(&o)[4] = O[blk * 2 + u];
-                        o[0] = o[0] * f0 + c[0];
-                        o[1] = o[1] * f1 + c[1];
-                        o[2] = o[2] * f0 + c[2];
-                        o[3] = o[3] * f1 + c[3];
+                for (int blk = 0; blk < D / 32; ++blk) {
+                    float c[2][4] = {};
+#pragma unroll
+                    for (int u = 0; u < KT; ++u) {
+                        uint32_t bp[2][2];
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            const float2 s0 = unpack2(vsc[u][2 * n][blk / 2], __half());
+                            const float2 s1 = unpack2(vsc[u][2 * n + 1][blk / 2], __half());
+                            const float u0 = p[u][2 * n] * (blk & 1 ? s0.y : s0.x);
+                            const float u1 = p[u][2 * n + 1] * (blk & 1 ? s1.y : s1.x);
+                            bp[0][n] = pack2(u0, u1, H());
+                            const float2 hf = unpack2(bp[0][n], H());
+                            bp[1][n] = pack2(u0 - hf.x, u1 - hf.y, H());
+                            if constexpr (NH == 4)  // columns 4-7 carry the second piece
+                                bp[0][n] = g < 4 ? bp[0][n] : bp[1][n];
+                        }
+                        uint32_t w[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            w[x] = lds32(S::column(vb + (u * kGroup + (x >> 1) * 8) * S::RS +
+                                                       val_row[x & 1], blk)) ^ 0x80808080u;
+                        const uint32_t e01 = __byte_perm(w[0], w[1], 0x5140),
+                                       e23 = __byte_perm(w[0], w[1], 0x7362),
+                                       o01 = __byte_perm(w[2], w[3], 0x5140),
+                                       o23 = __byte_perm(w[2], w[3], 0x7362);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t a0 = codes_f16(h ? e23 : e01, 0x4140);
+                            const uint32_t a1 = codes_f16(h ? e23 : e01, 0x4342);
+                            const uint32_t a2 = codes_f16(h ? o23 : o01, 0x4140);
+                            const uint32_t a3 = codes_f16(h ? o23 : o01, 0x4342);
+                            if constexpr (NH == 8)
+                                mma<KIND>(c[h], a0, a1, a2, a3, bp[1][0], bp[1][1]);
+                            mma<KIND>(c[h], a0, a1, a2, a3, bp[0][0], bp[0][1]);
+                        }
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float(&o)[4] = O[blk * 2 + h];
+                        o[0] = o[0] * f0 + c[h][0];
+                        o[1] = o[1] * f1 + c[h][1];
+                        o[2] = o[2] * f0 + c[h][2];
+                        o[3] = o[3] * f1 + c[h][3];
                     }
                 }
             } else {
                 constexpr int PIECES = KIND == kBF16 ? 3 : 2;
                 constexpr int MMAS = NH == 4 ? PIECES - 1 : PIECES;
-                uint32_t b[PIECES][2];
+                uint32_t b[KT][PIECES][2];
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    float u0 = p[2 * n], u1 = p[2 * n + 1];
+                for (int u = 0; u < KT; ++u)
 #pragma unroll
-                    for (int q = 0; q < PIECES; ++q) {
-                        b[q][n] = pack2(u0, u1, H());
-                        const float2 hf = unpack2(b[q][n], H());
-                        u0 -= hf.x;
-                        u1 -= hf.y;
+                    for (int n = 0; n < 2; ++n) {
+                        float u0 = p[u][2 * n], u1 = p[u][2 * n + 1];
+#pragma unroll
+                        for (int q = 0; q < PIECES; ++q) {
+                            b[u][q][n] = pack2(u0, u1, H());
+                            const float2 hf = unpack2(b[u][q][n], H());
+                            u0 -= hf.x;
+                            u1 -= hf.y;
+                        }
+                        if constexpr (NH == 4) {  // columns 4-7 carry the second piece
+                            b[u][0][n] = g < 4 ? b[u][0][n] : b[u][1][n];
+                            if constexpr (PIECES == 3)
+                                b[u][1][n] = g < 4 ? b[u][2][n] : 0u;
+                        }
                     }
-                    if constexpr (NH == 4) {  // columns 4-7 carry the second piece
-                        b[0][n] = g < 4 ? b[0][n] : b[1][n];
-                        if constexpr (PIECES == 3)
-                            b[1][n] = g < 4 ? b[2][n] : 0u;
-                    }
-                }
-                const uint32_t vaddr = vb + frag_row;
 #pragma unroll
                 for (int ds = 0; ds < S::KSTEPS; ++ds) {
-                    uint32_t a[4];
-                    ldsm4t(a, S::chunk_at(vaddr, ds));
                     float c[4] = {};
 #pragma unroll
-                    for (int q = MMAS - 1; q >= 0; --q)
-                        mma<KIND>(c, a[0], a[1], a[2], a[3], b[q][0], b[q][1]);
+                    for (int u = 0; u < KT; ++u) {
+                        uint32_t a[4];
+                        ldsm4t(a, S::column(vb + u * kGroup * S::RS + frag_row, ds));
+#pragma unroll
+                        for (int q = MMAS - 1; q >= 0; --q)
+                            mma<KIND>(c, a[0], a[1], a[2], a[3], b[u][q][0], b[u][q][1]);
+                    }
                     O[ds][0] = O[ds][0] * f0 + c[0];
                     O[ds][1] = O[ds][1] * f1 + c[1];
                     O[ds][2] = O[ds][2] * f0 + c[2];
@@ -969,9 +1035,9 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
                 odd |= !(fabsf(O[ds][x]) <= FLT_MAX);
         if (__any_sync(0xffffffffu, odd)) {
             float inf[D / 16][2] = {};  // sum of the column's infinities and NaNs
-            for (int i = 0; i < nw * kTile; ++i) {
+            for (int i = 0; i < nw * TILE; ++i) {
                 uint32_t row;
-                if (!row_of((sp.t0 + ta + warp + i / kTile * kWarps) * kTile + i % kTile, row))
+                if (!row_of((sp.t0 + ta + warp + i / TILE * kWarps) * TILE + i % TILE, row))
                     continue;
 #pragma unroll
                 for (int ds = 0; ds < D / 16; ++ds)
@@ -1182,12 +1248,11 @@ cudaError_t launch_heads(AttnParams &p, int sm_count, cudaStream_t s)
         return cudaErrorInvalidConfiguration;
     p.head_tiles = (p.group + NH - 1) / NH;
     p.items = p.a.c.n_heads * p.head_tiles;
-    p.min_units = kMinUnits;
     const int64_t longest = std::min<int64_t>(p.a.ld_table * p.a.c.page_size, 0x7fffffe0);
     const int64_t items = int64_t(p.a.n_seqs) * p.items;
-    const int64_t units = items * ((longest + kTile - 1) / kTile + 1 + kItemCost);
+    const int64_t units = items * ((longest + Sh::TILE - 1) / Sh::TILE + 1 + Sh::COST);
     int64_t grid = std::min<int64_t>(int64_t(occ) * sm_count, p.a.max_blocks);
-    grid = std::max<int64_t>(1, std::min(grid, std::max(items, units / p.min_units) + 1));
+    grid = std::max<int64_t>(1, std::min(grid, std::max(items, units / Sh::MIN_UNITS) + 1));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(grid));
     cfg.blockDim = dim3(Sh::THREADS);

@@ -473,7 +473,6 @@ struct AttnParams {
     int group;          // query heads per kv head
     int head_tiles;     // ceil(group / heads of a tile)
     int items;          // kv heads * head tiles
-    int min_units;      // units (16-key tiles, and kItemCost an item) a block takes at least
 };
 bool attn_takes_head_dim(int D);
 size_t attn_partial_floats(int D);  // floats of one partial result
