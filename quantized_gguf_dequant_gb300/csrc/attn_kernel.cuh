@@ -56,13 +56,6 @@ namespace qmm {
 
 namespace {
 
-#ifndef ATTN_TWO
-#define ATTN_TWO 64
-#define ATTN_Q8_TWO 128
-#endif
-#ifndef ATTN_W
-#define ATTN_W 4
-#endif
 constexpr int kGroup = 16;  // keys of an instruction group (the instruction's k and two n)
 constexpr int kLens = 512;  // lengths kept in shared memory
 // The fixed part of an item's time in a block (its first loads, its joins), in
@@ -76,16 +69,14 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 enum Kind { kF16, kBF16, kQ8 };
 
-// Warps of a block.
-constexpr int attn_warps(Kind, int) { return ATTN_W; }
 // Groups of a tile, the keys a warp takes in one step.  Two share the step's
 // fixed instructions and its latency where shared memory still holds enough
 // warps' stages.
-constexpr int attn_groups(Kind k, int D) { return k == kQ8 ? (D <= ATTN_Q8_TWO ? 2 : 1) : (D <= ATTN_TWO ? 2 : 1); }
+constexpr int attn_groups(Kind k, int D) { return k == kQ8 && D <= 128 ? 2 : 1; }
 
-template <Kind KIND, int D, int NH>
+template <Kind KIND, int D, int NH, int WARPS>
 struct Shape {
-    static constexpr int W = attn_warps(KIND, D), THREADS = 32 * W;
+    static constexpr int W = WARPS, THREADS = 32 * W;
     static constexpr int KT = attn_groups(KIND, D), TILE = KT * kGroup;
     static constexpr unsigned ALL = KT == 2 ? 0xffffffffu : 0xffffu;  // every key valid
     static constexpr int COST = kItemCost / KT, MIN_UNITS = kMinUnits / KT;  // in tiles
@@ -323,11 +314,12 @@ __device__ __forceinline__ float value_at(const uint8_t *data, const void *scale
         return load1(reinterpret_cast<const Half<KIND> *>(data) + row * D + d);
 }
 
-template <Kind KIND, int D, int NH>
-__global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH>::BLOCKS)
+template <Kind KIND, int D, int NH, int WARPS>
+__global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
+                                  Shape<KIND, D, NH, WARPS>::BLOCKS)
     attn_kernel(const __grid_constant__ AttnParams P)
 {
-    using S = Shape<KIND, D, NH>;
+    using S = Shape<KIND, D, NH, WARPS>;
     constexpr int kWarps = S::W, kThreads = S::THREADS, KT = S::KT, TILE = S::TILE;
     using H = Half<KIND>;
     constexpr int STAGES = S::STAGES;
@@ -337,6 +329,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
     __shared__ int64_t found_at;   // first tile of the sequence that the block starts in
     __shared__ int found_seq;
     __shared__ int lens[kLens];
+    __shared__ unsigned strides[32];
     __shared__ unsigned valid_ring[kWarps][STAGES];
     __shared__ int qexp[NH];
     __shared__ bool qfinite[NH];
@@ -351,7 +344,10 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
     pdl_launch_dependents();
 
     // ---- the plan: prefix sums of the sequences' units
-    auto units_of = [&](int n) { return n ? int64_t(n + S::COST) * P.items : int64_t(0); };
+    // An item's units (and, up to 32 sequences, what rounds them up to whole shares).
+    int round = 0;
+    auto stride_of = [&](int n) { return n ? unsigned(n + S::COST) : 0u; };
+    auto units_of = [&](int n) { return int64_t(stride_of(n)) * P.items; };
     auto len_of = [&](int b) { return b < kLens ? lens[b] : __ldg(A.lens + b); };
     // Sequences without keys are no one's item: their outputs are zero.
     auto fill_empty = [&]() {
@@ -378,6 +374,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
     };
     int64_t total = 0, per, r0, seq_at;
     int seq, seq_len;
+    unsigned seq_stride;  // units of an item of the sequence
     if (A.n_seqs <= 32) {
         // every warp by itself, a sequence a lane
         const int len = lane < A.n_seqs ? __ldg(A.lens + lane) : 0;
@@ -386,19 +383,43 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
             atomicOr(A.status, kStatusBadLengthBit);
         if (warp == 0)
             lens[lane] = len;  // (read after later barriers)
-        const int64_t mine = units_of(sp.n);
-        int64_t upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-            upto += lane >= o ? v : 0;
-        }
-        total = __shfl_sync(0xffffffffu, upto, 31);
+        const unsigned own = stride_of(sp.n);
+        // (2^27 tiles a sequence at most: sums of 32 fit 32 bits)
+        total = int64_t(__reduce_add_sync(0xffffffffu, own)) * P.items;
         if (total == 0) {
             fill_empty();
             return;
         }
         per = share(total, __reduce_max_sync(0xffffffffu, sp.n));
+        // With fewer items than blocks, shares a little larger may let every
+        // block keep to one item: a second one costs it another start and join.
+        unsigned stride = own;
+        if (per < (1 << 23) && __reduce_max_sync(0xffffffffu, own) < (1u << 23)) {
+            const unsigned p0 = unsigned(per);
+            for (unsigned more = 0; more <= 4; more += 2) {
+                const unsigned p = p0 + p0 * more / 16u;
+                unsigned parts = unsigned(__fdividef(float(own), float(p)));
+                parts += parts * p < own;  // (rounded down or exact: up)
+                if (uint64_t(__reduce_add_sync(0xffffffffu, parts)) * unsigned(P.items) <=
+                    gridDim.x) {
+                    round = int(p);
+                    stride = parts * p;
+                    break;
+                }
+            }
+            if (round)
+                per = round;
+        }
+        if (warp == 0)
+            strides[lane] = stride;  // (read after later barriers)
+        unsigned sum = stride;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned v = __shfl_up_sync(0xffffffffu, sum, o);
+            sum += lane >= o ? v : 0u;
+        }
+        const int64_t upto = int64_t(sum) * P.items, mine = int64_t(stride) * P.items;
+        total = __shfl_sync(0xffffffffu, upto, 31);
         r0 = per * blockIdx.x;
         const unsigned past = __ballot_sync(0xffffffffu, upto > r0);
         if (!past) {
@@ -408,6 +429,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
         seq = __ffs(past) - 1;
         seq_at = __shfl_sync(0xffffffffu, upto - mine, seq);
         seq_len = __shfl_sync(0xffffffffu, len, seq);
+        seq_stride = __shfl_sync(0xffffffffu, stride, seq);
     } else {
         for (int b = tid; b < min(A.n_seqs, kLens); b += kThreads)
             lens[b] = __ldg(A.lens + b);
@@ -469,6 +491,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
         seq = found_seq;
         seq_at = found_at;
         seq_len = len_of(seq);
+        seq_stride = stride_of(tiles_of<TILE>(A, seq_len).n);
     }
     const int64_t blk = blockIdx.x, r1 = min(total, r0 + per);
     Span sp = tiles_of<TILE>(A, seq_len);
@@ -490,17 +513,18 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
     float *join_ml = join + kWarps * NH * S::OSTRIDE;
 
     for (int64_t at = r0; at < r1;) {
-        while (at >= seq_at + units_of(sp.n)) {
-            seq_at += units_of(sp.n);
+        while (at >= seq_at + int64_t(seq_stride) * P.items) {
+            seq_at += int64_t(seq_stride) * P.items;
             ++seq;
             sp = tiles_of<TILE>(A, len_of(seq));
+            seq_stride = round ? strides[seq] : stride_of(sp.n);
         }
         // the item and this block's tiles [ta, tb) of it
-        const int item = int(uint64_t(at - seq_at) / unsigned(sp.n + S::COST));
-        const int64_t tiles_at = seq_at + int64_t(item) * (sp.n + S::COST) + S::COST;
+        const int item = int(uint64_t(at - seq_at) / seq_stride);
+        const int64_t item_at = seq_at + int64_t(item) * seq_stride, tiles_at = item_at + S::COST;
         const int ta = int(max(int64_t(0), at - tiles_at));
         const int tb = int(max(int64_t(0), min(r1 - tiles_at, int64_t(sp.n))));
-        at = tiles_at + sp.n;
+        at = item_at + seq_stride;
         if (tb <= ta)
             break;  // the range ends in the item's overhead: the next block starts the item
         const int kvh = item / P.head_tiles, h0 = (item % P.head_tiles) * NH;
@@ -1231,11 +1255,11 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH>::THREADS, Shape<KIND, D, NH
     fill_empty();
 }
 
-template <Kind KIND, int D, int NH>
-cudaError_t launch_heads(AttnParams &p, int sm_count, cudaStream_t s)
+template <Kind KIND, int D, int NH, int WARPS>
+cudaError_t launch_warps(AttnParams &p, int sm_count, cudaStream_t s)
 {
-    using Sh = Shape<KIND, D, NH>;
-    const auto kern = attn_kernel<KIND, D, NH>;
+    using Sh = Shape<KIND, D, NH, WARPS>;
+    const auto kern = attn_kernel<KIND, D, NH, WARPS>;
     const void *f = reinterpret_cast<const void *>(kern);
     cudaError_t e = func_smem(f, Sh::SMEM, true);
     if (e != cudaSuccess)
@@ -1264,6 +1288,25 @@ cudaError_t launch_heads(AttnParams &p, int sm_count, cudaStream_t s)
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 1 : 0;
     return counted(cudaLaunchKernelEx(&cfg, kern, p));
+}
+
+// Warps of a block.  Narrow rows: eight, two blocks on an SM (24 sequences of
+// 1024 keys, head_dim 64: 16.7 us, with four warps 20).  16-bit rows of 128: four,
+// three blocks, which overlap one another's starts and joins; with few items, whose
+// parts all have to be joined, one block of twelve (one sequence of 131071 keys:
+// 50.5 us, with four 53.5; 337 keys: 7.0 us, with four 8.0).
+template <Kind KIND, int D, int NH>
+cudaError_t launch_heads(AttnParams &p, int sm_count, cudaStream_t s)
+{
+    if constexpr (KIND != kQ8 && D == 64)
+        return launch_warps<KIND, D, NH, 8>(p, sm_count, s);
+    if constexpr (KIND != kQ8 && D == 128) {
+        const int64_t items =
+            int64_t(p.a.n_seqs) * p.a.c.n_heads * ((p.group + NH - 1) / NH);
+        if (items * 4 <= sm_count)
+            return launch_warps<KIND, D, NH, 12>(p, sm_count, s);
+    }
+    return launch_warps<KIND, D, NH, 4>(p, sm_count, s);
 }
 
 // Up to four heads that share a key: their pieces of q and of the
