@@ -44,6 +44,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 #include <cfloat>
 #include <cstring>
 #include <type_traits>
@@ -74,9 +75,11 @@ enum Kind { kF16, kBF16, kQ8 };
 // warps' stages.
 constexpr int attn_groups(Kind k, int D) { return k == kQ8 && D <= 128 ? 2 : 1; }
 
-template <Kind KIND, int D, int NH, int WARPS>
+template <Kind KIND, int D, int HEADS, int WARPS>
 struct Shape {
     static constexpr int W = WARPS, THREADS = 32 * W;
+    // heads of an operand, and operands of the block's heads
+    static constexpr int NH = HEADS < 8 ? HEADS : 8, HT = HEADS / NH;
     static constexpr int KT = attn_groups(KIND, D), TILE = KT * kGroup;
     static constexpr unsigned ALL = KT == 2 ? 0xffffffffu : 0xffffu;  // every key valid
     static constexpr int COST = kItemCost / KT, MIN_UNITS = kMinUnits / KT;  // in tiles
@@ -102,9 +105,9 @@ struct Shape {
     // q's operand registers in shared memory: four a lane (two pieces of eight
     // heads, or up to four of four), and two for a third piece of eight heads
     static constexpr bool THIRD = KIND == kBF16 && NH == 8;
-    static constexpr int QFRAG = KSTEPS * (THIRD ? 768 : 512);
+    static constexpr int QF1 = KSTEPS * (THIRD ? 768 : 512), QFRAG = HT * QF1;
     static constexpr int OSTRIDE = D + 4;
-    static constexpr int JOIN = W * NH * (OSTRIDE + 2) * 4;
+    static constexpr int JOIN = W * HEADS * (OSTRIDE + 2) * 4;
     // Resident blocks an SM: as many as leave two stages a warp (and, for the
     // registers, four): a warp's work on a tile is a chain of dependent
     // steps that other warps have to cover.
@@ -314,12 +317,13 @@ __device__ __forceinline__ float value_at(const uint8_t *data, const void *scale
         return load1(reinterpret_cast<const Half<KIND> *>(data) + row * D + d);
 }
 
-template <Kind KIND, int D, int NH, int WARPS>
-__global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
-                                  Shape<KIND, D, NH, WARPS>::BLOCKS)
+template <Kind KIND, int D, int HEADS, int WARPS>
+__global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
+                                  Shape<KIND, D, HEADS, WARPS>::BLOCKS)
     attn_kernel(const __grid_constant__ AttnParams P)
 {
-    using S = Shape<KIND, D, NH, WARPS>;
+    using S = Shape<KIND, D, HEADS, WARPS>;
+    constexpr int NH = S::NH, HT = S::HT;
     constexpr int kWarps = S::W, kThreads = S::THREADS, KT = S::KT, TILE = S::TILE;
     using H = Half<KIND>;
     constexpr int STAGES = S::STAGES;
@@ -331,9 +335,9 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
     __shared__ int lens[kLens];
     __shared__ unsigned strides[32];
     __shared__ unsigned valid_ring[kWarps][STAGES];
-    __shared__ int qexp[NH];
-    __shared__ bool qfinite[NH];
-    __shared__ float q_off[NH][D / 32];
+    __shared__ int qexp[HEADS];
+    __shared__ bool qfinite[HEADS];
+    __shared__ float q_off[HEADS][D / 32];
     __shared__ bool last_block;
 
     const AttnArgs &A = P.a;
@@ -510,7 +514,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
     const bool whole_groups = C.page.d % kGroup == 0;  // a group lies in one page
     const uint32_t ring = smem_base + S::QFRAG + warp * STAGES * S::STAGE;
     float *join = reinterpret_cast<float *>(smem + S::QFRAG);
-    float *join_ml = join + kWarps * NH * S::OSTRIDE;
+    float *join_ml = join + kWarps * HEADS * S::OSTRIDE;
 
     for (int64_t at = r0; at < r1;) {
         while (at >= seq_at + int64_t(seq_stride) * P.items) {
@@ -527,8 +531,8 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
         at = item_at + seq_stride;
         if (tb <= ta)
             break;  // the range ends in the item's overhead: the next block starts the item
-        const int kvh = item / P.head_tiles, h0 = (item % P.head_tiles) * NH;
-        const int nh = min(NH, P.group - h0);
+        const int kvh = item / P.head_tiles, h0 = (item % P.head_tiles) * HEADS;
+        const int nh = min(HEADS, P.group - h0);
         const int head0 = kvh * P.group + h0;  // first query head
         const int nw = max(0, (tb - ta - warp + kWarps - 1) / kWarps);  // this warp's tiles
         const int32_t *table = A.table + int64_t(seq) * A.ld_table;
@@ -628,24 +632,25 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
             }
             cp_commit();
         };
-        // q of head tid/16, issued ahead of everything that waits
-        float qv[D / 16];
-        {
-            const int h = tid >> 4;
+        // q of heads tid/16 and 8 more, issued ahead of everything that waits
+        float qv[HT][D / 16];
+#pragma unroll
+        for (int hh = 0; hh < HT; ++hh) {
+            const int h = (tid >> 4) + hh * 8;
             const int64_t q0 =
                 int64_t(seq) * A.ldq + int64_t(head0 + min(h, nh - 1)) * D + (tid & 15);
             if (A.dtype == QMM_F32) {
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i)
-                    qv[i] = __ldg(static_cast<const float *>(A.q) + q0 + i * 16);
+                    qv[hh][i] = __ldg(static_cast<const float *>(A.q) + q0 + i * 16);
             } else if (A.dtype == QMM_F16) {
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i)
-                    qv[i] = load_io<__half>(A.q, q0 + i * 16);
+                    qv[hh][i] = load_io<__half>(A.q, q0 + i * 16);
             } else {
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i)
-                    qv[i] = load_io<__nv_bfloat16>(A.q, q0 + i * 16);
+                    qv[hh][i] = load_io<__nv_bfloat16>(A.q, q0 + i * 16);
             }
         }
         int next_id;
@@ -661,14 +666,15 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
         }
 
         // ---- q's pieces as A operands, by 16 threads a head
-        {
-            const int h = tid >> 4, lt = tid & 15;
+#pragma unroll
+        for (int hh = 0; hh < HT; ++hh) {
+            const int h = (tid >> 4) + hh * 8, lt = tid & 15;
             float mx = 0.f, sum = 0.f;  // sum: 0, or NaN where q is not finite
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
-                qv[i] = h < nh ? qv[i] : 0.f;
-                mx = fmaxf(mx, fabsf(qv[i]));
-                sum += qv[i] * 0.f;
+                qv[hh][i] = h < nh ? qv[hh][i] : 0.f;
+                mx = fmaxf(mx, fabsf(qv[hh][i]));
+                sum += qv[hh][i] * 0.f;
             }
             int e = 0;
 #pragma unroll
@@ -685,8 +691,9 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
                     qexp[h] = e;
                     qfinite[h] = sum == 0.f;
                 }
-                uint16_t *frag = reinterpret_cast<uint16_t *>(smem);
-                uint16_t *frag3 = reinterpret_cast<uint16_t *>(smem + S::KSTEPS * 512);
+                uint16_t *frag = reinterpret_cast<uint16_t *>(smem + hh * S::QF1);
+                uint16_t *frag3 =
+                    reinterpret_cast<uint16_t *>(smem + hh * S::QF1 + S::KSTEPS * 512);
                 const float f = exp2i(e);
                 float off[D / 32] = {};
 #pragma unroll
@@ -708,19 +715,20 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
                         frag[(ks * 32 + (r & 7) * 4 + tt) * 8 + (2 * hi + (r >> 3)) * 2 + (d & 1)] =
                             *reinterpret_cast<const uint16_t *>(&v);
                     };
-                    const float x = qv[i] * f;
+                    const float x = qv[hh][i] * f;
                     const H p0 = H(x);
                     const float r1 = x - float(p0);
                     const H p1 = H(r1);
                     off[i / 2] += float(p0) + float(p1);
-                    put(h, p0);
-                    put(h + NH, p1);
+                    const int hr = h & 7;  // the head's row of its operand
+                    put(hr, p0);
+                    put(hr + NH, p1);
                     if constexpr (NH == 4) {
-                        put(h + 8, KIND == kBF16 ? H(r1 - float(p1)) : H(0.f));
-                        put(h + 12, H(0.f));
+                        put(hr + 8, KIND == kBF16 ? H(r1 - float(p1)) : H(0.f));
+                        put(hr + 12, H(0.f));
                     } else if constexpr (S::THIRD) {
                         const H p2 = H(r1 - float(p1));
-                        frag3[(ks * 32 + h * 4 + tt) * 4 + hi * 2 + (d & 1)] =
+                        frag3[(ks * 32 + hr * 4 + tt) * 4 + hi * 2 + (d & 1)] =
                             *reinterpret_cast<const uint16_t *>(&p2);
                     }
                 }
@@ -738,23 +746,31 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
         }
         __syncthreads();
 
-        const int hd = g & (NH - 1);  // the head whose scores this lane holds
-        const float qscale =
-            A.scale * exp2i(-qexp[hd]) * (KIND == kQ8 ? 0x1p24f : 1.f);
-        float qoff[D / 32];
-        if constexpr (KIND == kQ8) {
+        const int hg = g & (NH - 1);  // the head of an operand whose scores this lane holds
+        float qscale[HT], slope[HT], qoff[HT][D / 32];
 #pragma unroll
-            for (int blk = 0; blk < D / 32; ++blk)
-                qoff[blk] = g < NH ? q_off[hd][blk] : 0.f;
+        for (int hh = 0; hh < HT; ++hh) {
+            const int hd = hh * 8 + hg;
+            qscale[hh] = A.scale * exp2i(-qexp[hd]) * (KIND == kQ8 ? 0x1p24f : 1.f);
+            slope[hh] = A.alibi && hd < nh ? __ldg(A.alibi + head0 + hd) * kLog2e : 0.f;
+            if constexpr (KIND == kQ8) {
+#pragma unroll
+                for (int blk = 0; blk < D / 32; ++blk)
+                    qoff[hh][blk] = g < NH ? q_off[hd][blk] : 0.f;
+            }
         }
         const float cap_inv = A.softcap > 0.f ? 1.f / A.softcap : 0.f;
-        const float slope =
-            A.alibi && hd < nh ? __ldg(A.alibi + head0 + hd) * kLog2e : 0.f;
         // f16 probabilities are carried 2^14 times as large, clear of its subnormals
         constexpr float kBias = KIND == kF16 ? 14.f : 0.f;
-        float m = -INFINITY, l = 0.f;  // of head hd
-        int vexp = -126;               // Q8_0: exponent of the largest value scale so far
-        float O[D / 16][4] = {};
+        float m[HT], l[HT];  // of head hd
+        int vexp[HT];        // Q8_0: exponent of the largest value scale so far
+        float O[HT][D / 16][4] = {};
+#pragma unroll
+        for (int hh = 0; hh < HT; ++hh) {
+            m[hh] = -INFINITY;
+            l[hh] = 0.f;
+            vexp[hh] = -126;
+        }
 
         auto key_in = [&](int x) { return 2 * t + (x & 1) + (x >> 1) * 8; };  // of a group
         for (int i = 0; i < nw; ++i) {
@@ -766,6 +782,10 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
             const uint32_t kb = ring + st * S::STAGE, vb = kb + TILE * S::RS;
             const uint32_t ksb = vb + TILE * S::RS, vsb = ksb + TILE * S::SCB;
 
+#pragma unroll
+            for (int hh = 0; hh < HT; ++hh) {
+            const int hd = hh * 8 + hg;
+            const uint8_t *const qs = smem + hh * S::QF1;
             // ---- scores of head hd at keys 2t, 2t+1, 2t+8, 2t+9 of each group
             float s[KT][4];
             if constexpr (KIND == kQ8) {
@@ -784,7 +804,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
                     uint4 a[2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint8_t *fr = smem + ((2 * blk + h) * 32 + lane) * 16;
+                        const uint8_t *fr = qs + ((2 * blk + h) * 32 + lane) * 16;
                         if constexpr (NH == 8) {
                             a[h] = *reinterpret_cast<const uint4 *>(fr);
                         } else {  // rows 8-15 are empty
@@ -798,7 +818,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
                     for (int u = 0; u < KT; ++u)
 #pragma unroll
                         for (int n = 0; n < 2; ++n) {
-                            float c[4] = {qoff[blk], qoff[blk], 0.f, 0.f};
+                            float c[4] = {qoff[hh][blk], qoff[hh][blk], 0.f, 0.f};
                             uint2 w = lds64(
                                 S::column(kb + (u * kGroup + n * 8) * S::RS + key_row, blk));
                             w.x ^= 0x80808080u;
@@ -821,10 +841,10 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
 #pragma unroll
                 for (int ks = 0; ks < S::KSTEPS; ++ks) {
                     const uint4 a =
-                        *reinterpret_cast<const uint4 *>(smem + (ks * 32 + lane) * 16);
+                        *reinterpret_cast<const uint4 *>(qs + (ks * 32 + lane) * 16);
                     uint2 a3 = make_uint2(0u, 0u);
                     if constexpr (S::THIRD)
-                        a3 = *reinterpret_cast<const uint2 *>(smem + S::KSTEPS * 512 +
+                        a3 = *reinterpret_cast<const uint2 *>(qs + S::KSTEPS * 512 +
                                                               (ks * 32 + lane) * 8);
 #pragma unroll
                     for (int u = 0; u < KT; ++u) {
@@ -888,17 +908,17 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
                 if (A.softcap > 0.f) {
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
-                        s[u][x] = A.softcap * kLog2e * tanhf(s[u][x] * qscale * cap_inv);
+                        s[u][x] = A.softcap * kLog2e * tanhf(s[u][x] * qscale[hh] * cap_inv);
                 } else {
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
-                        s[u][x] *= qscale * kLog2e;
+                        s[u][x] *= qscale[hh] * kLog2e;
                 }
                 if (A.alibi) {
                     const float back = float(key0 + u * kGroup + 2 * t - (sp.hi - 1));
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
-                        s[u][x] += slope * (back + float((x & 1) + (x >> 1) * 8));
+                        s[u][x] += slope[hh] * (back + float((x & 1) + (x >> 1) * 8));
                 }
                 if (valid != S::ALL) {
 #pragma unroll
@@ -909,10 +929,10 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
             }
             tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 1));
             tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 2));
-            const float mn = fmaxf(m, tmax);
+            const float mn = fmaxf(m[hh], tmax);
             const float base = mn == -INFINITY ? 0.f : mn;
-            const float corr = ex2(m - base);  // 0 while nothing was seen
-            m = mn;
+            const float corr = ex2(m[hh] - base);  // 0 while nothing was seen
+            m[hh] = mn;
             float p[KT][4], psum = 0.f;
 #pragma unroll
             for (int u = 0; u < KT; ++u)
@@ -921,7 +941,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
                     p[u][x] = ex2(s[u][x] - (base - kBias));
                     psum += p[u][x];
                 }
-            l = l * corr + psum;
+            l[hh] = l[hh] * corr + psum;
             // O's columns 2t and 2t+1 are heads (and with four heads, pieces)
             float f0 = __shfl_sync(0xffffffffu, corr, 8 * t),
                   f1 = __shfl_sync(0xffffffffu, corr, 8 * t + 4);
@@ -946,13 +966,13 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
                 float dm = __half2float(__hmax(__low2half(mx), __high2half(mx)));
                 dm = fmaxf(dm, __shfl_xor_sync(0xffffffffu, dm, 1));
                 dm = fmaxf(dm, __shfl_xor_sync(0xffffffffu, dm, 2));
-                int ve = max(vexp, int(__float_as_uint(dm) >> 23) - 127);
+                int ve = max(vexp[hh], int(__float_as_uint(dm) >> 23) - 127);
                 if (ve > 15)  // an infinite scale: the others keep theirs
-                    ve = vexp > -126 ? vexp : 15;
-                const float fe = exp2i(max(-126, vexp - ve));
+                    ve = vexp[hh] > -126 ? vexp[hh] : 15;
+                const float fe = exp2i(max(-126, vexp[hh] - ve));
                 f0 *= fe;
                 f1 *= fe;
-                vexp = ve;
+                vexp[hh] = ve;
                 const float up = exp2i(min(126, 14 - ve));
 #pragma unroll
                 for (int u = 0; u < KT; ++u)
@@ -999,7 +1019,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
                     }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        float(&o)[4] = O[blk * 2 + h];
+                        float(&o)[4] = O[hh][blk * 2 + h];
                         o[0] = o[0] * f0 + c[h][0];
                         o[1] = o[1] * f1 + c[h][1];
                         o[2] = o[2] * f0 + c[h][2];
@@ -1039,11 +1059,12 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
                         for (int q = MMAS - 1; q >= 0; --q)
                             mma<KIND>(c, a[0], a[1], a[2], a[3], b[u][q][0], b[u][q][1]);
                     }
-                    O[ds][0] = O[ds][0] * f0 + c[0];
-                    O[ds][1] = O[ds][1] * f1 + c[1];
-                    O[ds][2] = O[ds][2] * f0 + c[2];
-                    O[ds][3] = O[ds][3] * f1 + c[3];
+                    O[hh][ds][0] = O[hh][ds][0] * f0 + c[0];
+                    O[hh][ds][1] = O[hh][ds][1] * f1 + c[1];
+                    O[hh][ds][2] = O[hh][ds][2] * f0 + c[2];
+                    O[hh][ds][3] = O[hh][ds][3] * f1 + c[3];
                 }
+            }
             }
             __syncwarp();
         }
@@ -1053,10 +1074,12 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
         // any, are settled by looking at the values again.
         bool odd = false;
 #pragma unroll
-        for (int ds = 0; ds < D / 16; ++ds)
+        for (int hh = 0; hh < HT; ++hh)
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-                odd |= !(fabsf(O[ds][x]) <= FLT_MAX);
+            for (int ds = 0; ds < D / 16; ++ds)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    odd |= !(fabsf(O[hh][ds][x]) <= FLT_MAX);
         if (__any_sync(0xffffffffu, odd)) {
             float inf[D / 16][2] = {};  // sum of the column's infinities and NaNs
             for (int i = 0; i < nw * TILE; ++i) {
@@ -1072,14 +1095,19 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
                     }
             }
 #pragma unroll
-            for (int ds = 0; ds < D / 16; ++ds)
+            for (int hh = 0; hh < HT; ++hh)
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    if (!(fabsf(O[ds][x]) <= FLT_MAX) && inf[ds][x >> 1] != 0.f)
-                        O[ds][x] = inf[ds][x >> 1];
+                for (int ds = 0; ds < D / 16; ++ds)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        if (!(fabsf(O[hh][ds][x]) <= FLT_MAX) && inf[ds][x >> 1] != 0.f)
+                            O[hh][ds][x] = inf[ds][x >> 1];
         }
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
+#pragma unroll
+        for (int hh = 0; hh < HT; ++hh) {
+            l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 1);
+            l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 2);
+        }
         __syncthreads();  // every warp is done with its ring: it becomes the joining space
 
         // ---- the warps' results joined
@@ -1091,16 +1119,17 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
                 A.lse[int64_t(seq) * A.n_q + head0 + h] =
                     tot == 0.f ? -INFINITY : (M + log2f(tot) - kBias) * kLn2;
         };
-        {
+#pragma unroll
+        for (int hh = 0; hh < HT; ++hh) {
             float undo = 1.f;
             if constexpr (KIND == kQ8)
-                undo = exp2i(max(-126, vexp - 14));
-            float *o = join + warp * NH * S::OSTRIDE;
+                undo = exp2i(max(-126, vexp[hh] - 14));
+            float *o = join + (warp * HEADS + hh * 8) * S::OSTRIDE;
 #pragma unroll
             for (int ds = 0; ds < D / 16; ++ds) {
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    float v = O[ds][x];
+                    float v = O[hh][ds][x];
                     if constexpr (NH == 4)
                         v += __shfl_xor_sync(0xffffffffu, v, 2);
                     if (NH == 8 || t < 2)
@@ -1108,8 +1137,8 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
                 }
             }
             if (t == 0 && g < NH) {
-                join_ml[(warp * NH + g) * 2] = m;
-                join_ml[(warp * NH + g) * 2 + 1] = l;
+                join_ml[(warp * HEADS + hh * 8 + g) * 2] = m[hh];
+                join_ml[(warp * HEADS + hh * 8 + g) * 2 + 1] = l[hh];
             }
         }
         __syncthreads();
@@ -1117,7 +1146,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
         // blocks that share the item
         const int64_t c0 = whole ? blk : uint64_t(tiles_at) / uint64_t(per);
         const int64_t c1 = whole ? blk : uint64_t(tiles_at + sp.n - 1) / uint64_t(per);
-        constexpr int PART = NH * (D + 2);  // floats of a partial: [8][D] sums, [8] m, [8] l
+        constexpr int PART = HEADS * (D + 2);  // floats of a partial: sums, m and l of each head
         constexpr int QUADS = D / 4;
         // A block may be the last of one item and the first of another: a
         // partial that starts its item goes to the block's second place.
@@ -1127,7 +1156,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
             float mw[kWarps], M = -INFINITY;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                mw[w] = join_ml[(w * NH + h) * 2];
+                mw[w] = join_ml[(w * HEADS + h) * 2];
                 M = fmaxf(M, mw[w]);
             }
             float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1136,16 +1165,16 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
             for (int w = 0; w < kWarps; ++w) {
                 const float f = mw[w] == -INFINITY ? 0.f : ex2(mw[w] - M);
                 add4(sum, f, *reinterpret_cast<const float4 *>(
-                                 join + (w * NH + h) * S::OSTRIDE + d));
-                tot += f * join_ml[(w * NH + h) * 2 + 1];
+                                 join + (w * HEADS + h) * S::OSTRIDE + d));
+                tot += f * join_ml[(w * HEADS + h) * 2 + 1];
             }
             if (whole) {
                 finish(h, d, sum, M, tot);
             } else {
                 __stcg(reinterpret_cast<float4 *>(mine_ws + h * D + d), sum);
                 if (d == 0) {
-                    __stcg(mine_ws + NH * D + h, M);
-                    __stcg(mine_ws + NH * D + NH + h, tot);
+                    __stcg(mine_ws + HEADS * D + h, M);
+                    __stcg(mine_ws + HEADS * D + HEADS + h, tot);
                 }
             }
         }
@@ -1188,8 +1217,8 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
                     for (int j = 0; j < 16; ++j) {
                         const float *w = place(from + min(c + j, count - 1) * step);
                         o[j] = __ldcg(reinterpret_cast<const float4 *>(w + h * D + d));
-                        pm[j] = c + j < count ? __ldcg(w + NH * D + h) : -INFINITY;
-                        pl[j] = __ldcg(w + NH * D + NH + h);
+                        pm[j] = c + j < count ? __ldcg(w + HEADS * D + h) : -INFINITY;
+                        pl[j] = __ldcg(w + HEADS * D + HEADS + h);
                     }
                     float mn = M;
 #pragma unroll
@@ -1213,7 +1242,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
             bool mine_to_join = last_of(
                 A.tickets + (grp ? A.max_blocks + c0 + first : c0), size);
             if (mine_to_join && gs < n) {
-                constexpr int PER = (NH * QUADS + kThreads - 1) / kThreads;
+                constexpr int PER = (HEADS * QUADS + kThreads - 1) / kThreads;
                 float4 sum[PER];
                 float M[PER], tot[PER];
 #pragma unroll
@@ -1231,8 +1260,8 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
                         continue;
                     __stcg(reinterpret_cast<float4 *>(w + h * D + d), sum[u]);
                     if (d == 0) {
-                        __stcg(w + NH * D + h, M[u]);
-                        __stcg(w + NH * D + NH + h, tot[u]);
+                        __stcg(w + HEADS * D + h, M[u]);
+                        __stcg(w + HEADS * D + HEADS + h, tot[u]);
                     }
                 }
                 mine_to_join = last_of(A.tickets + 2 * A.max_blocks + c0, (n + gs - 1) / gs);
@@ -1255,22 +1284,28 @@ __global__ void __launch_bounds__(Shape<KIND, D, NH, WARPS>::THREADS,
     fill_empty();
 }
 
-template <Kind KIND, int D, int NH, int WARPS>
+template <Kind KIND, int D, int HEADS, int WARPS>
 cudaError_t launch_warps(AttnParams &p, int sm_count, cudaStream_t s)
 {
-    using Sh = Shape<KIND, D, NH, WARPS>;
-    const auto kern = attn_kernel<KIND, D, NH, WARPS>;
-    const void *f = reinterpret_cast<const void *>(kern);
-    cudaError_t e = func_smem(f, Sh::SMEM, true);
-    if (e != cudaSuccess)
-        return e;
-    int occ = 0;
-    e = func_occupancy(f, Sh::THREADS, Sh::SMEM, &occ);
-    if (e != cudaSuccess)
-        return e;
-    if (occ < 1)
-        return cudaErrorInvalidConfiguration;
-    p.head_tiles = (p.group + NH - 1) / NH;
+    using Sh = Shape<KIND, D, HEADS, WARPS>;
+    const auto kern = attn_kernel<KIND, D, HEADS, WARPS>;
+    // Resident blocks of an SM, asked for once a device.
+    static std::atomic<int> resident[64];
+    const unsigned dev = unsigned(p.a.device);
+    int occ = dev < 64 ? resident[dev].load(std::memory_order_relaxed) : 0;
+    if (occ == 0) {
+        const void *f = reinterpret_cast<const void *>(kern);
+        cudaError_t e = func_smem(f, Sh::SMEM, true);
+        if (e == cudaSuccess)
+            e = func_occupancy(f, Sh::THREADS, Sh::SMEM, &occ);
+        if (e != cudaSuccess)
+            return e;
+        if (occ < 1)
+            return cudaErrorInvalidConfiguration;
+        if (dev < 64)
+            resident[dev].store(occ, std::memory_order_relaxed);
+    }
+    p.head_tiles = (p.group + HEADS - 1) / HEADS;
     p.items = p.a.c.n_heads * p.head_tiles;
     const int64_t longest = std::min<int64_t>(p.a.ld_table * p.a.c.page_size, 0x7fffffe0);
     const int64_t items = int64_t(p.a.n_seqs) * p.items;
@@ -1295,28 +1330,37 @@ cudaError_t launch_warps(AttnParams &p, int sm_count, cudaStream_t s)
 // three blocks, which overlap one another's starts and joins; with few items, whose
 // parts all have to be joined, one block of twelve (one sequence of 131071 keys:
 // 50.5 us, with four 53.5; 337 keys: 7.0 us, with four 8.0).
-template <Kind KIND, int D, int NH>
+template <Kind KIND, int D, int HEADS>
 cudaError_t launch_heads(AttnParams &p, int sm_count, cudaStream_t s)
 {
     if constexpr (KIND != kQ8 && D == 64)
-        return launch_warps<KIND, D, NH, 8>(p, sm_count, s);
-    if constexpr (KIND != kQ8 && D == 128) {
+        return launch_warps<KIND, D, HEADS, 8>(p, sm_count, s);
+    if constexpr (KIND != kQ8 && D == 128 && HEADS <= 8) {
         const int64_t items =
-            int64_t(p.a.n_seqs) * p.a.c.n_heads * ((p.group + NH - 1) / NH);
+            int64_t(p.a.n_seqs) * p.a.c.n_heads * ((p.group + HEADS - 1) / HEADS);
         if (items * 4 <= sm_count)
-            return launch_warps<KIND, D, NH, 12>(p, sm_count, s);
+            return launch_warps<KIND, D, HEADS, 12>(p, sm_count, s);
     }
-    return launch_warps<KIND, D, NH, 4>(p, sm_count, s);
+    return launch_warps<KIND, D, HEADS, 4>(p, sm_count, s);
 }
 
-// Up to four heads that share a key: their pieces of q and of the
-// probabilities fill the operands' other four rows and columns, half the
-// instructions of the eight-head form.
+// Heads that a block takes together.  Up to four that share a key: their pieces
+// of q and of the probabilities fill the operands' other four rows and columns,
+// half the instructions of the eight-head form.  Over eight: sixteen, so that
+// keys and values are fetched once for them, where the second operand's
+// instructions and registers cost less than the second fetch out of L2 (16
+// sequences of 4096 keys, 16 heads a key: head_dim 64 in f16 28 us, bf16 35, with
+// eight heads 37 and 40; f16 128: 51, with eight 55; bf16 128: 57, with eight 55).
 template <Kind KIND, int D>
 cudaError_t launch_dim(AttnParams &p, int sm_count, cudaStream_t s)
 {
-    return p.group <= 4 ? launch_heads<KIND, D, 4>(p, sm_count, s)
-                        : launch_heads<KIND, D, 8>(p, sm_count, s);
+    if (p.group <= 4)
+        return launch_heads<KIND, D, 4>(p, sm_count, s);
+    if constexpr ((KIND != kQ8 && D == 64) || (KIND == kF16 && D == 128)) {
+        if (p.group > 8)
+            return launch_heads<KIND, D, 16>(p, sm_count, s);
+    }
+    return launch_heads<KIND, D, 8>(p, sm_count, s);
 }
 
 template <Kind KIND>

@@ -447,6 +447,7 @@ qmm_status qmm_attn_decode(qmm_kv_t h, int32_t dtype, int64_t n_seqs, int32_t n_
         a.tickets = c.tickets;
         a.status = c.status;
         a.max_blocks = c.max_blocks;
+        a.device = c.device;
         const cudaError_t e =
             qmm::launch_attn_decode(a, c.sm_count, static_cast<cudaStream_t>(stream));
         return e == cudaSuccess ? QMM_OK : cuda_error(e, fn);

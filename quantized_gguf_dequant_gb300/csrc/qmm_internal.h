@@ -449,7 +449,7 @@ struct KvReadArgs {
 cudaError_t launch_kv_read(const KvReadArgs &a, int sm_count, cudaStream_t s);
 
 // Attention of one new token per sequence (attn_decode.cu).
-constexpr int kAttnHeads = 8;  // query heads of one kv head that a block takes at most
+constexpr int kAttnHeads = 16;  // query heads of one kv head that a block takes at most
 struct AttnArgs {
     KvView c;
     int type, dtype;
@@ -466,7 +466,7 @@ struct AttnArgs {
     float *lse;
     float *ws;
     unsigned *tickets, *status;
-    int max_blocks;
+    int max_blocks, device;
 };
 struct AttnParams {
     AttnArgs a;
