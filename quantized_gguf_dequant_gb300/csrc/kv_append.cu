@@ -27,11 +27,9 @@ namespace qmm {
 
 namespace {
 
-#ifndef APPEND_BLOCKS
-#define APPEND_BLOCKS 4
-#endif
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kThreads = 64, kWarps = kThreads / 32;  // of an append block
+constexpr int kAppendBlocks = 14;  // resident blocks of an SM, at least (for the registers)
+constexpr int kReadThreads = 256;
 
 enum Kind { kF16, kBF16, kQ8 };
 
@@ -167,7 +165,7 @@ __device__ __forceinline__ void put(const KvView &c, bool isk, int64_t row, int 
 // is: (u, u + half the rotated chunks) for halves, then consecutive chunks of
 // what passes through; (u, u + half the row's chunks) for adjacent pairs.
 template <Kind KIND, typename IO, int D>
-__global__ void __launch_bounds__(kThreads, APPEND_BLOCKS) append_kernel(const __grid_constant__ AppendArgs P)
+__global__ void __launch_bounds__(kThreads, kAppendBlocks) append_kernel(const __grid_constant__ AppendArgs P)
 {
     constexpr int N = Chunk<IO>::N;
     constexpr int LPR = D / N / 2;      // lanes per row
@@ -351,7 +349,7 @@ constexpr int kReadTokens = 64;  // of a block, at most
 constexpr int kReadUnits = 4;    // chunks of a thread under way at once
 
 template <Kind KIND, typename IO>
-__global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ KvReadArgs P)
+__global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ KvReadArgs P)
 {
     constexpr int N = Chunk<IO>::N;
     using H = typename std::conditional<KIND == kBF16, __nv_bfloat16, __half>::type;
@@ -379,7 +377,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
     }
     __syncthreads();
     const int units = n * int(P.unit.d);
-    for (int i0 = threadIdx.x; i0 < units; i0 += kReadUnits * kThreads) {
+    for (int i0 = threadIdx.x; i0 < units; i0 += kReadUnits * kReadThreads) {
         uint2 raw[2][kReadUnits] = {};  // 4 or 8 codes, or 4 values of 16 bits
         uint2 more[2][kReadUnits] = {}; // 8 values of 16 bits: the second half
         __half scale[2][kReadUnits];
@@ -388,7 +386,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
         bool held[kReadUnits];
 #pragma unroll
         for (int u = 0; u < kReadUnits; ++u) {
-            const int i = min(i0 + u * kThreads, units - 1);
+            const int i = min(i0 + u * kReadThreads, units - 1);
             const int t = int(fast_div(P.unit, unsigned(i)));
             const int in = i - t * int(P.unit.d);
             const int head = int(fast_div(P.chunk, unsigned(in)));
@@ -425,7 +423,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
         }
 #pragma unroll
         for (int u = 0; u < kReadUnits; ++u) {
-            if (i0 + u * kThreads >= units)
+            if (i0 + u * kReadThreads >= units)
                 continue;
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
@@ -459,11 +457,11 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
 }
 
 template <typename Args>
-cudaError_t launch(void (*k)(Args), dim3 grid, cudaStream_t s, const Args &a)
+cudaError_t launch(void (*k)(Args), dim3 grid, int threads, cudaStream_t s, const Args &a)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(unsigned(threads));
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -498,13 +496,13 @@ cudaError_t append_for_dim(const AppendArgs &a, int sm_count, cudaStream_t s)
     const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(passes, 4 * sm_count / a.T));
     const dim3 grid(unsigned(a.T), unsigned(parts));
     if (!regular)
-        return launch(append_any_kernel<KIND, IO>, grid, s, a);
+        return launch(append_any_kernel<KIND, IO>, grid, kThreads, s, a);
     switch (a.c.D) {
-    case 64: return launch(append_kernel<KIND, IO, 64>, grid, s, a);
-    case 96: return launch(append_kernel<KIND, IO, 96>, grid, s, a);
-    case 128: return launch(append_kernel<KIND, IO, 128>, grid, s, a);
-    case 192: return launch(append_kernel<KIND, IO, 192>, grid, s, a);
-    case 256: return launch(append_kernel<KIND, IO, 256>, grid, s, a);
+    case 64: return launch(append_kernel<KIND, IO, 64>, grid, kThreads, s, a);
+    case 96: return launch(append_kernel<KIND, IO, 96>, grid, kThreads, s, a);
+    case 128: return launch(append_kernel<KIND, IO, 128>, grid, kThreads, s, a);
+    case 192: return launch(append_kernel<KIND, IO, 192>, grid, kThreads, s, a);
+    case 256: return launch(append_kernel<KIND, IO, 256>, grid, kThreads, s, a);
     }
     return cudaErrorInvalidValue;
 }
@@ -524,9 +522,9 @@ template <Kind KIND>
 cudaError_t read_for_io(const KvReadArgs &a, dim3 grid, cudaStream_t s)
 {
     switch (a.dtype) {
-    case QMM_F32: return launch(read_kernel<KIND, float>, grid, s, a);
-    case QMM_F16: return launch(read_kernel<KIND, __half>, grid, s, a);
-    case QMM_BF16: return launch(read_kernel<KIND, __nv_bfloat16>, grid, s, a);
+    case QMM_F32: return launch(read_kernel<KIND, float>, grid, kReadThreads, s, a);
+    case QMM_F16: return launch(read_kernel<KIND, __half>, grid, kReadThreads, s, a);
+    case QMM_BF16: return launch(read_kernel<KIND, __nv_bfloat16>, grid, kReadThreads, s, a);
     }
     return cudaErrorInvalidValue;
 }
@@ -552,7 +550,7 @@ cudaError_t launch_kv_read(const KvReadArgs &args, int sm_count, cudaStream_t s)
     // tokens of a block: what its threads ask for at once, fewer while there
     // are SMs without a block
     a.tokens = int(std::max<int64_t>(
-        1, std::min({int64_t(kReadUnits * kThreads) / units, (a.T + sm_count - 1) / sm_count,
+        1, std::min({int64_t(kReadUnits * kReadThreads) / units, (a.T + 4 * sm_count - 1) / (4 * sm_count),
                      int64_t(kReadTokens)})));
     const dim3 grid(unsigned((a.T + a.tokens - 1) / a.tokens));
     switch (a.type) {
