@@ -359,82 +359,33 @@ class Matrix:
 
 # ------------------------------------------------- the decode step around the products
 
-# These calls are small next to what Python spends on them: checks are plain
-# attribute reads, and what they need of torch and of the library is looked up
-# once (_ops).
-class _Ops:
-    """torch, its dtypes, and the C entries, looked up on first use."""
+NATIVE_PATH = os.path.join(_HERE, "_native.so")
+_native = None
 
-    def __init__(self):
-        import torch
+
+def native():
+    """The module behind the calls below (csrc/binding.cpp): it takes tensors
+    apart, checks them and calls the C ABI of the loaded library."""
+    global _native
+    if _native is None:
+        import importlib.machinery
+        import importlib.util
+
+        import torch  # noqa: F401  (its libraries must be loaded first)
         L = lib()
-        self.torch, self.empty = torch, torch.empty
-        self.f32, self.i32, self.i64 = torch.float32, torch.int32, torch.int64
-        self.ids = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
-        self.append, self.read, self.attn = L.qmm_kv_append, L.qmm_kv_read, L.qmm_attn_decode
-        self.logits = L.qmm_logits_adjust
-        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-    def type_id(self, dtype) -> int:
-        n = self.ids.get(dtype)
-        if n is None:
-            raise ValueError(f"{dtype} is not supported (float32, float16 and bfloat16 are)")
-        return n
-
-    def stream(self, stream, device):
-        if stream is None:
-            if self.raw_stream is not None:
-                return self.raw_stream(device)
-            stream = self.torch.cuda.current_stream(device)
-        return stream if isinstance(stream, int) else stream.cuda_stream
-
-
-_the_ops = None
-
-
-def _ops() -> _Ops:
-    global _the_ops
-    if _the_ops is None:
-        _the_ops = _Ops()
-    return _the_ops
-
-
-def _flat(t, name: str, dtype, n=None):
-    """The pointer of a contiguous device tensor of a torch dtype (and, with n
-    given, of n elements); None stays None."""
-    if t is None:
-        return None
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor on the CUDA device")
-    if n is not None and t.numel() != n:
-        raise ValueError(f"{name} has {t.numel()} elements; {n} are needed")
-    return t.data_ptr()
-
-
-def _heads(t, name: str, shape, dtype):
-    """Elements between the tokens of a [T, heads, D] tensor whose tokens may
-    lie apart, such as a slice of a fused projection's output."""
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}; {tuple(shape)} is needed")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} is {t.dtype}; {dtype} is needed")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must live on the CUDA device")
-    T, heads, D = shape
-    a, b, c = t.stride()
-    if c != 1 or (b != D and heads > 1):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return a if T > 1 else heads * D
-
-
-def _made_on(stream, *tensors):
-    """Outputs allocated here for work on a stream that is not the current one
-    must not return to the allocator before that work is done."""
-    if not isinstance(stream, int):
-        for t in tensors:
-            t.record_stream(stream)
+        if not os.path.exists(NATIVE_PATH):
+            raise RuntimeError(
+                f"{NATIVE_PATH} is missing: build it with "
+                "`python -m quantized_gguf_dequant_gb300.build` (there is no fallback)")
+        loader = importlib.machinery.ExtensionFileLoader("_native", NATIVE_PATH)
+        spec = importlib.util.spec_from_file_location("_native", NATIVE_PATH, loader=loader)
+        m = importlib.util.module_from_spec(spec)
+        loader.exec_module(m)
+        m.init(QmmError, *(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
+            "qmm_kv_append", "qmm_kv_read", "qmm_attn_decode", "qmm_logits_adjust",
+            "qmm_last_error")))
+        _native = m
+    return _native
 
 
 class Rope:
@@ -443,24 +394,27 @@ class Rope:
     a pair: "halves" (i, i + n_rot/2) or "adjacent" (2i, 2i + 1)."""
 
     def __init__(self, inv_freq, sections=None, pairing: str = "halves"):
+        import torch
         n = inv_freq.numel()
         sections = [n] if sections is None else [int(x) for x in sections]
         if pairing not in ("halves", "adjacent"):
             raise ValueError(f"pairing {pairing!r}: 'halves' or 'adjacent'")
         if not 1 <= len(sections) <= 4 or sum(sections) != n:
             raise ValueError(f"sections {sections} must be 1 to 4 counts that sum to {n} pairs")
+        if inv_freq.dtype != torch.float32 or not inv_freq.is_cuda or not inv_freq.is_contiguous():
+            raise ValueError("inv_freq must be a contiguous float32 tensor on the CUDA device")
         self.inv_freq = inv_freq  # keep the device memory alive
-        self.n_axes = len(sections)
         self.desc = RopeDesc(2 * n, int(pairing == "adjacent"), len(sections),
-                             (ctypes.c_int32 * 4)(*sections),
-                             _flat(inv_freq, "inv_freq", _ops().f32))
-        self.ref = ctypes.byref(self.desc)
+                             (ctypes.c_int32 * 4)(*sections), inv_freq.data_ptr())
+        self.address = ctypes.addressof(self.desc)
 
 
 class KVCache:
     """A paged key-value cache on the device (qmm_kv_create) with the calls
     that use it.  kind: F16, BF16 or Q8_0.  k, v: its two buffers (any dtype,
-    at least kv_bytes() bytes each); made and zeroed here when not given."""
+    at least kv_bytes() bytes each); made and zeroed here when not given.
+    Every call takes a stream (a torch stream or a raw handle; default: the
+    current one)."""
 
     def __init__(self, kind: int, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int,
                  k=None, v=None):
@@ -477,17 +431,16 @@ class KVCache:
                 raise ValueError(f"the {name} buffer holds {t.numel() * t.element_size()} bytes; "
                                  f"{need} are needed")
         self.k, self.v = k, v  # keep the buffers alive as long as the handle
+        self._native = native()
         h = ctypes.c_void_p()
         _check(lib().qmm_kv_create(kind, n_pages, page_size, n_kv_heads, head_dim, _ptr(k),
                                    _ptr(v), ctypes.byref(h)))
         self.h = h.value
-        self._ops, self._device = _ops(), k.device.index or 0
-        self._desc = AttnDesc()  # filled anew by each call (a handle serves one stream)
-        self._desc_ref = ctypes.byref(self._desc)
+        self._cache = self._native.cache(self.h, k.device.index or 0, n_kv_heads, head_dim)
 
     def close(self):
         if getattr(self, "h", None):
-            h, self.h = self.h, None
+            h, self.h, self._cache = self.h, None, None
             _check(lib().qmm_kv_destroy(h))
 
     def __del__(self):
@@ -500,33 +453,7 @@ class KVCache:
         """qmm_kv_append: rotate q and k ([T, heads, head_dim]) and store k and
         v at slots ([T] int64).  pos: [n_axes, T] (or [T]) int32.  Returns the
         rotated q (into q_out, which may be q), or None without q."""
-        o, D, dtype = self._ops, self.head_dim, k.dtype
-        T = k.shape[0]
-        shape = (T, self.n_kv_heads, D)
-        ldk, ldv = _heads(k, "k", shape, dtype), _heads(v, "v", shape, dtype)
-        qp = qop = pp = desc = None
-        ldq = ldqo = n_q = 0
-        if q is not None:
-            n_q = q.shape[1]
-            shape = (T, n_q, D)
-            ldq = _heads(q, "q", shape, dtype)
-            if q_out is None:
-                q_out = o.empty(shape, dtype=dtype, device=q.device)
-                ldqo = n_q * D
-                if stream is not None:
-                    _made_on(stream, q_out)
-            else:
-                ldqo = _heads(q_out, "q_out", shape, dtype)
-            qp, qop = q.data_ptr(), q_out.data_ptr()
-        if rope is not None:
-            pp = _flat(pos, "pos", o.i32, rope.n_axes * T)
-            desc = rope.ref
-        rc = o.append(self.h, o.type_id(dtype), T, k.data_ptr(), ldk, v.data_ptr(), ldv,
-                      _flat(slots, "slots", o.i64, T), qp, ldq, n_q, qop, ldqo, pp, desc,
-                      o.stream(stream, self._device))
-        if rc:
-            _check(rc)
-        return q_out if q is not None else None
+        return self._native.append(self._cache, k, v, slots, q, pos, rope, q_out, stream)
 
     def attend(self, q, page_table, lens, scale=None, softcap: float = 0.0, window: int = 0,
                alibi=None, out=None, lse=None, return_lse: bool = False, stream=None):
@@ -534,68 +461,12 @@ class KVCache:
         [n_seqs, n_q_heads, head_dim]; page_table: [n_seqs, pages] int32; lens:
         [n_seqs] int32; scale: 1/sqrt(head_dim) by default.  Returns out (like
         q), and with return_lse also lse ([n_seqs, n_q_heads] float32)."""
-        o = self._ops
-        shape, dtype = q.shape, q.dtype
-        if len(shape) != 3 or shape[2] != self.head_dim:
-            raise ValueError(f"q has shape {tuple(shape)}; [n_seqs, heads, {self.head_dim}] is needed")
-        B, n_q, D = shape
-        ldq = _heads(q, "q", shape, dtype)
-        if out is None:
-            out = o.empty(shape, dtype=dtype, device=q.device)
-            ldo = n_q * D
-            if stream is not None:
-                _made_on(stream, out)
-        else:
-            ldo = _heads(out, "out", shape, dtype)
-        lp = None
-        if lse is not None:
-            lp = _flat(lse, "lse", o.f32, B * n_q)
-        elif return_lse:
-            lse = o.empty((B, n_q), dtype=o.f32, device=q.device)
-            lp = lse.data_ptr()
-            if stream is not None:
-                _made_on(stream, lse)
-        if page_table.dim() != 2 or page_table.shape[0] != B:
-            raise ValueError(f"page_table must be [{B}, pages]")
-        if page_table.dtype is not o.i32 or not page_table.is_cuda:
-            raise ValueError("page_table must be int32 on the CUDA device")
-        if not page_table.is_contiguous():  # (the ABI takes a row's length as its stride)
-            raise ValueError("page_table must be contiguous")
-        d = self._desc
-        d.scale = D ** -0.5 if scale is None else scale
-        d.softcap, d.window = softcap, window
-        d.alibi = None if alibi is None else _flat(alibi, "alibi", o.f32, n_q)
-        rc = o.attn(self.h, o.type_id(dtype), B, n_q, q.data_ptr(), ldq, page_table.data_ptr(),
-                    page_table.shape[1], _flat(lens, "lens", o.i32, B), self._desc_ref,
-                    out.data_ptr(), ldo, lp, o.stream(stream, self._device))
-        if rc:
-            _check(rc)
-        return (out, lse) if return_lse else out
+        return self._native.attend(self._cache, q, page_table, lens, scale, softcap, window, alibi,
+                                   out, lse, return_lse, stream)
 
     def read(self, slots, dtype=None, k_out=None, v_out=None, stream=None):
         """qmm_kv_read: (k, v) values of the slots, [T, n_kv_heads, head_dim]."""
-        o = self._ops
-        T, D = slots.numel(), self.head_dim
-        shape = (T, self.n_kv_heads, D)
-        dtype = dtype or (k_out.dtype if k_out is not None else o.f32)
-        ldk = ldv = self.n_kv_heads * D
-        if k_out is None:
-            k_out = o.empty(shape, dtype=dtype, device=slots.device)
-            if stream is not None:
-                _made_on(stream, k_out)
-        else:
-            ldk = _heads(k_out, "k_out", shape, dtype)
-        if v_out is None:
-            v_out = o.empty(shape, dtype=dtype, device=slots.device)
-            if stream is not None:
-                _made_on(stream, v_out)
-        else:
-            ldv = _heads(v_out, "v_out", shape, dtype)
-        rc = o.read(self.h, o.type_id(dtype), T, _flat(slots, "slots", o.i64), k_out.data_ptr(),
-                    ldk, v_out.data_ptr(), ldv, o.stream(stream, self._device))
-        if rc:
-            _check(rc)
-        return k_out, v_out
+        return self._native.read(self._cache, slots, dtype, k_out, v_out, stream)
 
     def status(self) -> int:
         """The handle's device status (0 = OK); clears it."""
@@ -617,55 +488,6 @@ def logits_adjust(logits, out=None, *, history=None, history_offsets=None, repea
     one row of) logits.  history, bias_ids: int32, ragged by the rows + 1 int64
     offsets; repeat, presence, frequency: float32 [rows]; mask: int32 words
     [rows, words], or one row [words] for all.  out may be logits."""
-    o = _ops()
-    shape, dtype, stride = logits.shape, logits.dtype, logits.stride()
-    if len(shape) not in (1, 2) or not logits.is_cuda or (stride[-1] != 1 and shape[-1] > 1):
-        raise ValueError("logits must be [rows, vocabulary] or [vocabulary] on the CUDA device, "
-                         "each row contiguous")
-    B, V = shape if len(shape) == 2 else (1, shape[0])
-    ld = ldo = V
-    if out is None:
-        out = o.empty(shape, dtype=dtype, device=logits.device)
-        if stream is not None:
-            _made_on(stream, out)
-    else:
-        if out.shape != shape or out.dtype is not dtype or not out.is_cuda or \
-                (out.stride(-1) != 1 and V > 1):
-            raise ValueError("out must be like logits")
-        if B > 1:
-            ldo = out.stride(0)
-    if B > 1:
-        ld = stride[0]
-    r = LogitRules()
-    f32, i32, i64 = o.f32, o.i32, o.i64
-    if history is not None:
-        n = history.numel()
-        if n:
-            r.history = _flat(history, "history", i32)
-            r.history_offsets = _flat(history_offsets, "history_offsets", i64, B + 1)
-            r.n_history = n
-    if repeat is not None:
-        r.repeat = _flat(repeat, "repeat", f32, B)
-    if presence is not None:
-        r.presence = _flat(presence, "presence", f32, B)
-    if frequency is not None:
-        r.frequency = _flat(frequency, "frequency", f32, B)
-    if bias_ids is not None:
-        n = bias_ids.numel()
-        if n:
-            r.bias_ids = _flat(bias_ids, "bias_ids", i32)
-            r.bias_values = _flat(bias_values, "bias_values", f32, n)
-            r.bias_offsets = _flat(bias_offsets, "bias_offsets", i64, B + 1)
-            r.n_biases = n
-    if mask is not None:
-        words, n = mask.shape[-1], mask.numel()
-        if words * 32 < V or (n != words and n != B * words):
-            raise ValueError(f"mask of shape {tuple(mask.shape)} does not hold {B} or 1 rows of "
-                             f"{V} bits")
-        r.mask = _flat(mask, "mask", i32)
-        r.ld_mask = words if n == B * words else 0
-    rc = o.logits(o.type_id(dtype), B, V, logits.data_ptr(), ld, ctypes.byref(r), out.data_ptr(),
-                  ldo, o.stream(stream, logits.device.index))
-    if rc:
-        _check(rc)
-    return out
+    return (_native or native()).logits(logits, out, history, history_offsets, repeat, presence,
+                                        frequency, bias_ids, bias_values, bias_offsets, mask,
+                                        stream)

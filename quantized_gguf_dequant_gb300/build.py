@@ -1,21 +1,25 @@
 """Build libqmm.so (the CUDA library behind include/qmm.h) in-tree.
 
 Every translation unit is compiled for sm_103a only, in parallel, then linked
-into one shared object next to this file.  `python -m
+into one shared object next to this file; the native part of the Python binding
+(host code) is compiled beside them.  `python -m
 quantized_gguf_dequant_gb300.build` does the same from a shell.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libqmm.so")
+NATIVE = os.path.join(HERE, "_native.so")  # the binding of the decode-step calls
 SOURCES = ["qmm_api.cu", "dequant.cu", "gemv.cu", "gemv_tc.cu", "qmm_noalloc.cu", "moe.cu", "gemm_tc.cu", "tmap.cu", "gemv_batched.cu", "formats.cu", "gemv_m1.cu", "q8k.cu", "formats_fast.cu", "gemv_tc5.cu", "moe_q8.cu", "decode_api.cu", "kv_append.cu", "attn_decode.cu", "attn_f16.cu", "attn_bf16.cu", "attn_q8.cu", "logits.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -46,10 +50,28 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
     return obj
 
 
+def _build_native() -> str:
+    """csrc/binding.cpp against torch's headers (host code only)."""
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = NATIVE + f".tmp.{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
+           "-fvisibility=hidden", "-D_GLIBCXX_USE_CXX11_ABI=1",
+           "-I" + os.path.join(ROOT, "include"), "-I" + os.path.join(torch_dir, "include"),
+           "-I" + os.path.join(cuda, "include"), "-I" + sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L" + os.path.join(torch_dir, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, NATIVE)
+    return NATIVE
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(NATIVE):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(NATIVE))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     deps.append(os.path.join(ROOT, "include", "qmm.h"))
     deps.append(os.path.abspath(__file__))
@@ -60,8 +82,10 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if not (force or verbose_ptxas or _stale()):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        native = ex.submit(_build_native)
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), SOURCES))
+        native.result()
     tmp = LIB + f".tmp.{os.getpid()}"
     cmd = [nvcc(), "-shared", "-o", tmp] + objs + ARCH + ["-Xcompiler", "-fPIC"]
     r = subprocess.run(cmd, capture_output=True, text=True)
