@@ -188,47 +188,52 @@ __global__ void __launch_bounds__(kThreads, 5) adjust_kernel(const __grid_consta
     };
     for (int w0 = lo; w0 < hi; w0 += 32 * P.words) {
         const int span = min(hi - w0, 32 * P.words), words = (span + 31) / 32;
-        for (int i = tid; i < words; i += kThreads)
-            bitmap[i] = 0u;
+        // A short part counts at the tokens' own places instead of their ranks.
+        const bool direct = span <= kPlaces;
+        uint32_t total = uint32_t(span);
         if (tid == 0)
             twice = 0;
-        __syncthreads();
-        auto note = [&](int token) {
-            const unsigned at = unsigned(token) - unsigned(w0);
-            if (token >= 0 && at < unsigned(span))
-                atomicOr(bitmap + (at >> 5), 1u << (at & 31));
-        };
-        each_said(note);
-        each_bias([&](int token, uint32_t) { note(token); });
-        __syncthreads();
-        // ranks: a thread takes `run` consecutive words
-        const int run = (words + kThreads - 1) / kThreads;
-        uint32_t mine = 0;
-        for (int k = 0; k < run; ++k) {
-            const int i = tid * run + k;
-            if (i < words) {
-                before[i] = mine;
-                mine += __popc(bitmap[i]);
+        if (!direct) {
+            for (int i = tid; i < words; i += kThreads)
+                bitmap[i] = 0u;
+            __syncthreads();
+            auto note = [&](int token) {
+                const unsigned at = unsigned(token) - unsigned(w0);
+                if (token >= 0 && at < unsigned(span))
+                    atomicOr(bitmap + (at >> 5), 1u << (at & 31));
+            };
+            each_said(note);
+            each_bias([&](int token, uint32_t) { note(token); });
+            __syncthreads();
+            // ranks: a thread takes `run` consecutive words
+            const int run = (words + kThreads - 1) / kThreads;
+            uint32_t mine = 0;
+            for (int k = 0; k < run; ++k) {
+                const int i = tid * run + k;
+                if (i < words) {
+                    before[i] = mine;
+                    mine += __popc(bitmap[i]);
+                }
             }
-        }
-        uint32_t upto = mine;
+            uint32_t upto = mine;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
-            upto += lane >= o ? v : 0u;
-        }
-        if (lane == 31)
-            warp_sum_[tid >> 5] = upto;
-        __syncthreads();
-        uint32_t total = 0;
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
+                upto += lane >= o ? v : 0u;
+            }
+            if (lane == 31)
+                warp_sum_[tid >> 5] = upto;
+            __syncthreads();
+            total = 0;
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) {
-            upto += w < (tid >> 5) ? warp_sum_[w] : 0u;
-            total += warp_sum_[w];
+            for (int w = 0; w < kThreads / 32; ++w) {
+                upto += w < (tid >> 5) ? warp_sum_[w] : 0u;
+                total += warp_sum_[w];
+            }
+            for (int k = 0; k < run; ++k)
+                if (tid * run + k < words)
+                    before[tid * run + k] += upto - mine;
         }
-        for (int k = 0; k < run; ++k)
-            if (tid * run + k < words)
-                before[tid * run + k] += upto - mine;
         // named tokens by rank, kPlaces at a time
         for (uint32_t first = 0; first < total; first += kPlaces) {
             const uint32_t n = min(uint32_t(kPlaces), total - first);
@@ -241,6 +246,8 @@ __global__ void __launch_bounds__(kThreads, 5) adjust_kernel(const __grid_consta
                 const unsigned at = unsigned(token) - unsigned(w0);
                 if (token < 0 || at >= unsigned(span))
                     return uint32_t(kPlaces);
+                if (direct)
+                    return at;
                 return before[at >> 5] + __popc(bitmap[at >> 5] & ((1u << (at & 31)) - 1u)) - first;
             };
             each_said([&](int token) {
@@ -260,8 +267,10 @@ __global__ void __launch_bounds__(kThreads, 5) adjust_kernel(const __grid_consta
             });
             __syncthreads();
             for (uint32_t p = tid; p < n; p += kThreads) {
-                const int token = int(ids[p]);
                 const uint32_t c = counts[p], first_bias = owner[p];
+                if (direct && c == 0 && first_bias == kNoOwner)
+                    continue;
+                const int token = direct ? w0 + int(p) : int(ids[p]);
                 float z = load1(in + token);
                 const bool banned = mask && !(mask_bits(mask, token, V) & 1u);
                 if (c) {
