@@ -15,6 +15,12 @@
 // while the first rows' loads are already under way.  A lane holds its part of
 // a row in registers before it stores any of it, so q_out may be q.  A Q8_0
 // block of 32 values is eight lanes of fp32 or four of 16-bit values.
+// Small blocks, many to an SM: a block lives for about 2 us, most of it waiting
+// for its rows (256 threads instead of 64 took 24.5 us where these take 18.7).
+// Measured on one GB300: 4096 tokens of 32 + 8 + 8 heads of 128, bf16, three axes,
+// into f16: 18.7 us, 5.4 TB/s; 2011 tokens of fp32 into Q8_0 and back out: 22.6 us;
+// 16 tokens: 2.4 us; reading 16384 tokens of 8 heads out of Q8_0 in bf16: 18.4 us,
+// 5.6 TB/s; 301 tokens: 1.9 us.
 #include <algorithm>
 #include <cstring>
 #include <type_traits>

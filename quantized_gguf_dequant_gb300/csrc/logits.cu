@@ -17,6 +17,8 @@
 // which computes from the input.  Testing every logit against dense counts
 // instead takes three times the instructions of the stream itself and was
 // bound by issuing them (256 rows of 128256 logits: 67 us).
+// Measured on one GB300: those rows with 1000-2000 tokens of history, 100 biases
+// and a mask each: 56 us, 4.8 TB/s (41.5 us, 6.3 TB/s, without lists); one row: 3.8 us.
 // A bias list may name a token twice: the entry with the lowest index owns
 // the token and adds the others in list order, so the sum is repeatable.
 // Groups are taken at their 16-byte boundaries whatever the row's own
