@@ -1355,7 +1355,9 @@ cudaError_t launch_heads(AttnParams &p, int sm_count, cudaStream_t s)
         if (items * 4 <= sm_count)
             return launch_warps<KIND, D, HEADS, 12>(p, sm_count, s);
     }
-    return launch_warps<KIND, D, HEADS, 4>(p, sm_count, s);
+    // Rows of 96, and 16-bit rows of 256: six fill the shared memory better.
+    constexpr int W = D == 96 || (D == 256 && KIND != kQ8) ? 6 : 4;
+    return launch_warps<KIND, D, HEADS, W>(p, sm_count, s);
 }
 
 // Heads that a block takes together.  Up to four that share a key: their pieces
