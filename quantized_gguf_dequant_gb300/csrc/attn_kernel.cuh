@@ -79,7 +79,8 @@ constexpr int kItemCost = 12;
 // A block takes at least so much: splitting an item costs a join, which is
 // worth it from about twenty saved groups on.
 constexpr int kMinUnits = 36;
-constexpr int kStatic = 2560;  // the kernel's static shared memory, at most
+constexpr int kLaneSeqs = 4;  // sequences of a lane in the plan of some sequences
+constexpr int kStatic = 3072;  // the kernel's static shared memory, at most
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 enum Kind { kF16, kBF16, kQ8 };
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
     __shared__ int64_t found_at;   // first tile of the sequence that the block starts in
     __shared__ int found_seq;
     __shared__ int lens[kLens];
-    __shared__ unsigned strides[32];
+    __shared__ unsigned strides[32 * kLaneSeqs];
     __shared__ unsigned valid_ring[kWarps][STAGES];
     __shared__ int qexp[HEADS];
     __shared__ bool qfinite[HEADS];
@@ -362,7 +363,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
     pdl_launch_dependents();
 
     // ---- the plan: prefix sums of the sequences' units
-    // An item's units (and, up to 32 sequences, what rounds them up to whole shares).
+    // An item's units (and, for few sequences, what rounds them up to whole shares).
     int round = 0;
     auto stride_of = [&](int n) { return n ? unsigned(n + S::COST) : 0u; };
     auto units_of = [&](int n) { return int64_t(stride_of(n)) * P.items; };
@@ -448,7 +449,114 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
         seq_at = __shfl_sync(0xffffffffu, upto - mine, seq);
         seq_len = __shfl_sync(0xffffffffu, len, seq);
         seq_stride = __shfl_sync(0xffffffffu, stride, seq);
-    } else {
+    }
+    // Some more, none of astronomical length (sums fit 32 bits): the same with
+    // up to four neighbouring sequences a lane, where the general plan's barriers
+    // and loops cost more (128 sequences of 100 keys, 2 heads of 64: 11.4 -> 6.0 us;
+    // 48 of 1000, one head of 128: 14.9 -> 12.8).  Not for Q8_0: its kernel lost
+    // registers of the main loop to this (64 sequences: 276 -> 294 us).
+    bool some = KIND != kQ8 && A.n_seqs > 32 && A.n_seqs <= 32 * kLaneSeqs;
+    if (some) {
+        const int each = (A.n_seqs + 31) / 32;  // sequences of a lane
+        int len[kLaneSeqs];
+        unsigned stride[kLaneSeqs], own = 0;
+        int most = 0;
+#pragma unroll
+        for (int i = 0; i < kLaneSeqs; ++i) {
+            const int b = lane * each + i;
+            len[i] = i < each && b < A.n_seqs ? __ldg(A.lens + b) : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < kLaneSeqs; ++i) {
+            const Span sp = tiles_of<TILE>(A, len[i]);
+            if (blockIdx.x == 0 && warp == 0 && (len[i] < 0 || len[i] > sp.hi))
+                atomicOr(A.status, kStatusBadLengthBit);
+            if (warp == 0 && i < each)
+                lens[lane * each + i] = len[i];  // (read after later barriers)
+            stride[i] = stride_of(sp.n);
+            own += min(stride[i], 1u << 24);
+            most = max(most, sp.n);
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        some = most < (1 << 23);
+        total = int64_t(__reduce_add_sync(0xffffffffu, own)) * P.items;
+        if (total == 0) {
+            fill_empty();
+            return;
+        }
+        if (some) {
+            per = share(total, most);
+            // With someer items than blocks, shares a little larger may let every
+            // block keep to one item: a second one costs it another start and join.
+            if (per < (1 << 23)) {
+                const unsigned p0 = unsigned(per);
+                unsigned parts[kLaneSeqs];
+                for (unsigned more = 0; more <= 4 && !round; more += 2) {
+                    const unsigned p = p0 + p0 * more / 16u;
+                    unsigned sum = 0;
+#pragma unroll
+                    for (int i = 0; i < kLaneSeqs; ++i) {
+                        parts[i] = unsigned(__fdividef(float(stride[i]), float(p)));
+                        parts[i] += parts[i] * p < stride[i];  // (rounded down or exact: up)
+                        sum += parts[i];
+                    }
+                    if (uint64_t(__reduce_add_sync(0xffffffffu, sum)) * unsigned(P.items) <=
+                        gridDim.x)
+                        round = int(p);
+                }
+                if (round) {
+                    per = round;
+                    own = 0;
+#pragma unroll
+                    for (int i = 0; i < kLaneSeqs; ++i) {
+                        stride[i] = parts[i] * unsigned(round);
+                        own += stride[i];
+                    }
+                }
+            }
+            unsigned sum = own;  // of this lane's sequences and those before
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned v = __shfl_up_sync(0xffffffffu, sum, o);
+                sum += lane >= o ? v : 0u;
+            }
+            total = int64_t(__shfl_sync(0xffffffffu, sum, 31)) * P.items;
+            r0 = per * blockIdx.x;
+            const unsigned past = __ballot_sync(0xffffffffu, int64_t(sum) * P.items > r0);
+            if (!past) {
+                fill_empty();
+                return;
+            }
+            // the first of the lane's sequences that reaches past r0
+            unsigned at = sum - own;
+            int mine = 0;
+            bool found = false;
+#pragma unroll
+            for (int i = 0; i < kLaneSeqs; ++i) {
+                if (warp == 0 && i < each)
+                    strides[lane * each + i] = stride[i];  // (read after later barriers)
+                found |= int64_t(at + stride[i]) * P.items > r0;
+                if (!found) {
+                    at += stride[i];
+                    ++mine;
+                }
+            }
+            const int from = __ffs(past) - 1;
+            int my_len = len[0];
+            unsigned my_stride = stride[0];
+#pragma unroll
+            for (int i = 1; i < kLaneSeqs; ++i) {
+                my_len = mine == i ? len[i] : my_len;
+                my_stride = mine == i ? stride[i] : my_stride;
+            }
+            seq = from * each + __shfl_sync(0xffffffffu, mine, from);
+            seq_at = int64_t(__shfl_sync(0xffffffffu, at, from)) * P.items;
+            seq_len = __shfl_sync(0xffffffffu, my_len, from);
+            seq_stride = __shfl_sync(0xffffffffu, my_stride, from);
+        }
+    }
+    if (A.n_seqs > 32 && !some) {
+        total = 0;
         for (int b = tid; b < min(A.n_seqs, kLens); b += kThreads)
             lens[b] = __ldg(A.lens + b);
         __syncthreads();

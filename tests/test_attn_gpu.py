@@ -119,6 +119,44 @@ def test_more_sequences_than_threads(kind):
     check(kind, lens, 2, 2, 64, 16, seed=9)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("B,longest", [(32, 900), (33, 40), (33, 2500), (64, 700), (97, 60),
+                                       (128, 30), (128, 1500), (129, 300)])
+def test_counts_of_sequences(kind, B, longest):
+    rng = np.random.default_rng(B + longest)
+    lens = [int(n) for n in rng.integers(0, 40, B)]
+    lens[0] = lens[B // 2] = 0
+    lens[B - 1] = lens[B // 3] = longest
+    check(kind, lens, 1, 4, 64, 16, seed=B)
+
+
+def test_many_sequences_all_empty_but_the_last():
+    check("f16", [0] * 99 + [17], 2, 2, 64, 16)
+    check("f16", [0] * 77, 2, 2, 64, 16)
+
+
+def test_lengths_outside_the_table_are_cut_among_many():
+    rng = np.random.default_rng(21)
+    lens = [16] * 70
+    table, n_pages, slots = ref.table_for(lens, 16, rng)
+    pages = ref.Pages(q, "f16", n_pages, 16, 1, 64, rng)
+    cache = pages.to_device(np.concatenate(slots))
+    x = torch.from_numpy(rng.standard_normal((70, 2, 64)).astype(np.float32)).cuda()
+    run = lambda n: cache.attend(x, torch.from_numpy(table).cuda(), torch.tensor(
+        n, dtype=torch.int32, device="cuda"), scale=0.125)
+    want = run(lens)
+    assert cache.status() == q.OK
+    lens[41] = 1000  # past the table: as its 16 slots
+    got = run(lens)
+    assert torch.equal(got, want)
+    assert cache.status() != q.OK
+    lens[41], lens[69] = 16, -5  # below zero: empty
+    got = run(lens)
+    assert torch.equal(got[:69], want[:69]) and (got[69] == 0).all()
+    assert cache.status() != q.OK
+    cache.close()
+
+
 def test_all_sequences_empty():
     check("bf16", [0, 0, 0], 2, 2, 64, 16)
 
