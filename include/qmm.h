@@ -344,7 +344,7 @@ typedef struct qmm_kv_cache *qmm_kv_t;
  *     is padding and never read); value d = code[d] * scale[d/32].  Q8_0's
  *     blocks with the scales in a plane of their own.
  * Slot numbers are page * page_size + offset.  n_pages * page_size *
- * n_kv_heads <= 2^32 - 1.  Allocates the handle's workspace (the attention's
+ * n_kv_heads <= 2^32 - 1, n_kv_heads <= 2^20.  Allocates the handle's workspace (the attention's
  * partial results, about 5 MB at head_dim 128) and status word; synchronises.
  * Calls on one handle must be ordered on one stream, as for qmm_t.  No later
  * call allocates: they can be captured into a CUDA graph. */
@@ -416,7 +416,7 @@ typedef struct {
  * keys: out = sum_j softmax(s)_j v_j over the keys j in [max(0, len -
  * window), len), s_j = scale * q.k_j with the options above.  q, out:
  * [n_seqs, n_q_heads, head_dim] of one type, rows ldq, ldo elements apart on
- * 16-byte boundaries; head h reads kv head h / (n_q_heads / n_kv_heads).
+ * 16-byte boundaries and not overlapping; head h reads kv head h / (n_q_heads / n_kv_heads).
  * Key j of sequence b is slot page_table[b * ld_table + j / page_size] *
  * page_size + j % page_size; only the pages of keys in range are looked at.
  * lens[b] counts the new token's own key where it was appended before.  A
@@ -424,8 +424,8 @@ typedef struct {
  * n_q_heads] fp32, ln sum_j exp(s_j), -inf without keys (what joining with
  * attention over other keys needs).  Lengths are read on the device: a
  * captured call serves growing sequences.  A page id outside [0, n_pages)
- * leaves its keys out, a length that is negative or beyond ld_table pages is
- * cut to fit; either sets QMM_ERR_PAGE in the status word.  Slots out of
+ * leaves its keys out, a length that is negative or beyond ld_table pages (or
+ * 2^31 - 2^16 keys) is cut to fit; either sets QMM_ERR_PAGE in the status word.  Slots out of
  * range are never read, whatever they hold.
  * Computed in fp32 precision throughout (the cache's values are exact
  * operands); bitwise repeatable for the same lengths. */

@@ -79,6 +79,9 @@ constexpr int kItemCost = 12;
 // A block takes at least so much: splitting an item costs a join, which is
 // worth it from about twenty saved groups on.
 constexpr int kMinUnits = 36;
+// Keys of a sequence, at most: the units of 32 sequences fit 32 bits, and keys
+// past the last tile 31.
+constexpr int64_t kMostKeys = 0x7fff0000;
 constexpr int kLaneSeqs = 4;  // sequences of a lane in the plan of some sequences
 constexpr int kStatic = 3072;  // the kernel's static shared memory, at most
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -278,7 +281,7 @@ template <int TILE>
 __device__ __forceinline__ Span tiles_of(const AttnArgs &a, int len)
 {
     Span s;
-    s.hi = max(0, min(len, int(min(a.ld_table * a.c.page_size, int64_t(0x7fffffe0)))));
+    s.hi = max(0, min(len, int(min(a.ld_table * a.c.page_size, kMostKeys))));
     s.lo = a.window > 0 ? max(0, s.hi - a.window) : 0;
     s.t0 = s.lo / TILE;
     s.n = s.hi > s.lo ? (s.hi + TILE - 1) / TILE - s.t0 : 0;
@@ -403,7 +406,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
         if (warp == 0)
             lens[lane] = len;  // (read after later barriers)
         const unsigned own = stride_of(sp.n);
-        // (2^27 tiles a sequence at most: sums of 32 fit 32 bits)
+        // (kMostKeys: sums of 32 fit 32 bits)
         total = int64_t(__reduce_add_sync(0xffffffffu, own)) * P.items;
         if (total == 0) {
             fill_empty();
@@ -1429,7 +1432,7 @@ cudaError_t launch_warps(AttnParams &p, int sm_count, cudaStream_t s)
     }
     p.head_tiles = (p.group + HEADS - 1) / HEADS;
     p.items = p.a.c.n_heads * p.head_tiles;
-    const int64_t longest = std::min<int64_t>(p.a.ld_table * p.a.c.page_size, 0x7fffffe0);
+    const int64_t longest = std::min<int64_t>(p.a.ld_table * p.a.c.page_size, kMostKeys);
     const int64_t items = int64_t(p.a.n_seqs) * p.items;
     const int64_t units = items * ((longest + Sh::TILE - 1) / Sh::TILE + 1 + Sh::COST);
     int64_t grid = std::min<int64_t>(int64_t(occ) * sm_count, p.a.max_blocks);

@@ -9,6 +9,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
@@ -139,21 +140,27 @@ bool stream_of(PyObject *o, int device, void *&s)
     return !PyErr_Occurred();
 }
 
-// A new output.  What is made here for work on a stream that is not the
-// current one must not return to the allocator before that work is done.
-PyObject *output(at::IntArrayRef shape, at::ScalarType type, int device, PyObject *stream, void *&p)
+// A new output.  For work on a stream that is not the current one its memory
+// is that stream's (what the current stream still does with memory given back
+// is no concern of it), and is not given out again before the current stream,
+// which is likely to read it, has passed the point where it is dropped.
+PyObject *output(at::IntArrayRef shape, at::ScalarType type, int device, void *stream, void *&p)
 {
-    at::Tensor t = at::empty(
-        shape, at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, c10::DeviceIndex(device))));
-    p = t.data_ptr();
-    PyObject *o = THPVariable_Wrap(std::move(t));
-    if (o && stream != Py_None && !PyLong_Check(stream)) {
-        PyObject *r = PyObject_CallMethod(o, "record_stream", "O", stream);
-        if (!r)
-            Py_CLEAR(o);
-        Py_XDECREF(r);
+    const auto options =
+        at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, c10::DeviceIndex(device)));
+    const c10::cuda::CUDAStream current =
+        c10::cuda::getCurrentCUDAStream(c10::DeviceIndex(device));
+    at::Tensor t;
+    if (current.stream() == stream) {
+        t = at::empty(shape, options);
+    } else {
+        c10::cuda::CUDAStreamGuard on(c10::cuda::getStreamFromExternal(
+            static_cast<cudaStream_t>(stream), c10::DeviceIndex(device)));
+        t = at::empty(shape, options);
+        t.record_stream(current.unwrap());
     }
-    return o;
+    p = t.data_ptr();
+    return THPVariable_Wrap(std::move(t));
 }
 
 bool ok(qmm_status rc)
@@ -226,7 +233,7 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n)
                 return nullptr;
             out.borrow(a[7]);
         } else {
-            if (!(out.o = output({T, heads, c->D}, type, c->device, a[8], op)))
+            if (!(out.o = output({T, heads, c->D}, type, c->device, stream, op)))
                 return nullptr;
             ldo = heads * c->D;
         }
@@ -299,14 +306,14 @@ PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t n)
         if (!tokens(a[8], "out", B, heads, c->D, type, c->device, op, ldo))
             return nullptr;
         out.borrow(a[8]);
-    } else if (!(out.o = output({B, heads, c->D}, type, c->device, a[11], op))) {
+    } else if (!(out.o = output({B, heads, c->D}, type, c->device, stream, op))) {
         return nullptr;
     }
     if (a[9] != Py_None) {
         if (!flat(a[9], "lse", at::kFloat, B * heads, c->device, lp))
             return nullptr;
         lse.borrow(a[9]);
-    } else if (want && !(lse.o = output({B, heads}, at::kFloat, c->device, a[11], lp))) {
+    } else if (want && !(lse.o = output({B, heads}, at::kFloat, c->device, stream, lp))) {
         return nullptr;
     }
     const int64_t ld_table = table->size(1);
@@ -358,7 +365,7 @@ PyObject *read(PyObject *, PyObject *const *a, Py_ssize_t n)
                 return nullptr;
             out[w].borrow(a[3 + w]);
         } else {
-            if (!(out[w].o = output({T, c->heads, c->D}, type, c->device, a[5], p[w])))
+            if (!(out[w].o = output({T, c->heads, c->D}, type, c->device, stream, p[w])))
                 return nullptr;
             ld[w] = c->heads * c->D;
         }
@@ -415,7 +422,7 @@ PyObject *logits(PyObject *, PyObject *const *a, Py_ssize_t n)
             ldo = o->stride(0);
         op = o->data_ptr();
         out.borrow(a[1]);
-    } else if (!(out.o = output(shape, type, device, a[11], op))) {
+    } else if (!(out.o = output(shape, type, device, stream, op))) {
         return nullptr;
     }
     qmm_logit_rules r = {};

@@ -46,6 +46,9 @@ qmm_status cache_shape(const char *fn, int type, int64_t n_pages, int32_t page_s
     if (!qmm::attn_takes_head_dim(head_dim))
         return record_error(QMM_ERR_UNSUPPORTED, "%s: head_dim = %d is not implemented (64, 96, "
                             "128, 192 and 256 are)", fn, head_dim);
+    if (n_kv_heads > (1 << 20))
+        return record_error(QMM_ERR_SHAPE, "%s: n_kv_heads = %d; 2^20 at most are supported", fn,
+                            n_kv_heads);
     const int64_t per_page = int64_t(page_size) * n_kv_heads;
     if (per_page > INT_MAX || n_pages > int64_t(0xffffffffll) / per_page)
         return record_error(QMM_ERR_SHAPE, "%s: %lld pages x %d slots x %d heads exceed 2^32 - 1 "

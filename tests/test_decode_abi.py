@@ -50,6 +50,12 @@ def test_sizes(L, kind, D, row):
         q.kv_bytes(kind, 5, 7, 3, D + 1)
 
 
+def test_more_heads_than_fit_refuse():
+    assert q.kv_bytes(q.F16, 1, 1, 1 << 20, 64) == (1 << 20) * 128
+    with pytest.raises(q.QmmError, match="n_kv_heads"):
+        q.kv_bytes(q.F16, 1, 1, (1 << 20) + 1, 64)
+
+
 def test_null_handles_refuse(L):
     vp = ctypes.c_void_p
     assert L.qmm_kv_append(None, 0, 1, vp(16), 64, vp(16), 64, vp(16), None, 0, 0, None, 0, None,

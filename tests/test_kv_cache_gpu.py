@@ -217,6 +217,32 @@ def test_read(kind, io, D):
     assert cache.read(torch.from_numpy(slots[:0]).cuda())[0].shape == (0, 3, D)
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_outputs_on_another_stream(raw):
+    # what a call on another stream returns is that stream's memory: the
+    # current stream's next tensors cannot take its place while it is written
+    rng = np.random.default_rng(4)
+    cache = q.KVCache(q.F16, 20, 16, 2, 64)
+    x = torch.from_numpy(rng.standard_normal((300, 2, 64)).astype(np.float16)).cuda()
+    slots = torch.arange(300, device="cuda")
+    cache.append(x, x, slots)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    on = s.cuda_stream if raw else s
+    k, v = cache.read(slots, torch.float16, stream=on)
+    turned = cache.append(x, x, slots, q=x, stream=on)
+    y = q.logits_adjust(x.view(300, 128), stream=on)
+    s.synchronize()
+    assert torch.equal(k, x) and torch.equal(v, x)
+    assert torch.equal(turned, x) and torch.equal(y, x.view(300, 128))
+    torch.cuda.synchronize()
+    taken = {t.data_ptr() for t in (k, v, turned, y)}
+    del k, v, turned, y
+    new = [torch.empty((300, 2, 64), dtype=torch.float16, device="cuda") for _ in range(8)]
+    assert not taken & {t.data_ptr() for t in new}
+    cache.close()
+
+
 def test_refusals():
     cache = q.KVCache(q.F16, 2, 16, 2, 64)
     x = torch.randn(3, 2, 64, device="cuda")
