@@ -18,7 +18,7 @@
 // Small blocks, many to an SM: a block lives for about 2 us, most of it waiting
 // for its rows (256 threads instead of 64 took 24.5 us where these take 18.7).
 // Measured on one GB300: 4096 tokens of 32 + 8 + 8 heads of 128, bf16, three axes,
-// into f16: 18.7 us, 5.4 TB/s; 2011 tokens of fp32 into Q8_0 and back out: 22.6 us;
+// into f16: 18.6 us, 5.4 TB/s; 2011 tokens of fp32 into Q8_0 and back out: 20.9 us;
 // 16 tokens: 2.4 us; reading 16384 tokens of 8 heads out of Q8_0 in bf16: 18.4 us,
 // 5.6 TB/s; 301 tokens: 1.9 us.
 #include <algorithm>
@@ -85,28 +85,28 @@ template <int N>
 __device__ __forceinline__ void quantize(const float (&x)[N], uint32_t (&codes)[N / 4], float &d)
 {
     constexpr int LANES = 32 / N;
-    float amax = 0.f, nan = 0.f;
+    // The bits of |x| are in its order, a NaN's above infinity's.
+    uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        amax = fmaxf(amax, fabsf(x[i]));
-        nan += x[i] * 0.f;
-    }
+    for (int i = 0; i < N; ++i)
+        top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
 #pragma unroll
     for (int o = 1; o < LANES; o <<= 1)
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    // a NaN must reach the stored scale: fmaxf drops it
-    const unsigned bad = __ballot_sync(0xffffffffu, !(nan == 0.f) && !(amax == INFINITY));
-    if ((bad >> (threadIdx.x & (32 - LANES))) & ((1u << LANES) - 1))
-        amax = __int_as_float(0x7fc00000);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float amax = __uint_as_float(top);
     d = __fdiv_rn(amax, 127.f);
     const float inv = d > 0.f ? __fdiv_rn(1.f, d) : 0.f;
+    // At 1.5 * 2^23 a float's spacing is 1: the sum rounds to the code, in its
+    // low byte.  A block without a finite scale has codes of zero.
+    const uint32_t keep = inv > 0.f ? 0xffffffffu : 0u;
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
-        uint32_t w = 0;
+        uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            w |= (uint32_t(__float2int_rn(__fmul_rn(x[i + j], inv))) & 0xffu) << (8 * j);
-        codes[i / 4] = w;
+            w[j] = __float_as_uint(__fadd_rn(__fmul_rn(x[i + j], inv), 12582912.f));
+        codes[i / 4] = __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040),
+                                   0x5410) & keep;
     }
 }
 
@@ -273,8 +273,9 @@ __global__ void __launch_bounds__(kThreads, kAppendBlocks) append_kernel(const _
                     store_values<N>(qd + r * D + eb, b);
                 }
             }
-            // (Q8_0's blocks of 32 are neighbouring lanes' first, or second, chunks)
-            if (KIND == kQ8 || !isq) {
+            // (Q8_0's blocks of 32 are neighbouring lanes' first, or second, chunks:
+            // all lanes shuffle where any of the warp's rows is not q's)
+            if (KIND == kQ8 ? base + i * stride + RPW > P.n_q : !isq) {
                 const int head = isk ? r - P.n_q : r - P.n_q - c.n_heads;
                 const int64_t row = row0 + int64_t(head) * c.page_size;
                 const bool write = active && !isq && row0 >= 0;
@@ -288,63 +289,131 @@ __global__ void __launch_bounds__(kThreads, kAppendBlocks) append_kernel(const _
     }
 }
 
-// Any even number of rotated dims and any head size: a warp a row, every
-// element looks up its partner.
-template <Kind KIND, typename IO>
-__global__ void __launch_bounds__(kThreads) append_any_kernel(const __grid_constant__ AppendArgs P)
+// Any even number of rotated dims and any head size: a lane takes consecutive
+// chunks of a row, which the warp passes through shared memory, where every
+// chunk finds its partners.  A chunk is loaded and stored by the same lane, so
+// q_out may be q.  4096 tokens of 32 + 8 + 8 heads of 128 in bf16, half of each
+// rotated, into Q8_0 and back out: 31 us (append_kernel, all of each: 25); when
+// every element looked up its partner in global memory: 81.
+template <Kind KIND, typename IO, int PASSES>  // chunks of a lane in a row
+__global__ void __launch_bounds__(kThreads, kAppendBlocks) append_any_kernel(const __grid_constant__ AppendArgs P)
 {
     constexpr int N = Chunk<IO>::N;
-    constexpr int PASSES = (256 / N + 31) / 32;
+    constexpr int BATCH = 4 / PASSES;  // row groups under way at once
     __shared__ __align__(16) float2 turn[128];
+    __shared__ uint4 staged[kWarps][BATCH][PASSES * 32];
     pdl_wait();
     pdl_launch_dependents();
     const int64_t tok = blockIdx.x;
     const KvView &c = P.c;
-    const int D = c.D, half = P.n_rot >> 1;
+    const int D = c.D, half = P.n_rot >> 1, chunks = D / N;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rpw = max(1, 32 / chunks);  // rows of a warp
+    const int sub = chunks < 32 ? lane / chunks : 0, u = lane - sub * chunks;
     const int rows = P.n_q + 2 * c.n_heads;
+    const int stride = int(gridDim.y) * kWarps * rpw;
+    const bool aligned = half % N == 0;  // a chunk's partners are a chunk
+    const int64_t slot = __ldg(P.slots + tok);
+    Chunk<IO> x[BATCH][PASSES];
+    auto turned = [&](int r, int e) { return r < P.n_q + c.n_heads && e < P.n_rot; };
+    auto load = [&](int base) {
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const int r = base + i * stride + sub;
+            const bool isq = r < P.n_q, isk = !isq && r < P.n_q + c.n_heads;
+            const int head = isq ? r : (isk ? r - P.n_q : r - P.n_q - c.n_heads);
+            const IO *src = static_cast<const IO *>(isq ? P.q : (isk ? P.k : P.v)) +
+                            tok * (isq ? P.ldq : (isk ? P.ldk : P.ldv)) + head * D;
+#pragma unroll
+            for (int p = 0; p < PASSES; ++p) {
+                const int e = (p * 32 + u) * N;
+                x[i][p].raw = make_uint4(0, 0, 0, 0);
+                if (sub < rpw && r < rows && e < D)
+                    x[i][p].load(src + e);
+            }
+        }
+    };
+    int base = (int(blockIdx.y) * kWarps + warp) * rpw;
+    load(base);
     turns_of(P, tok, turn);
-    const int64_t row0 = row_of_slot(P, __ldg(P.slots + tok));
+    const int64_t row0 = row_of_slot(P, slot);
     __syncthreads();
-    for (int r = int(blockIdx.y) * kWarps + warp; r < rows; r += int(gridDim.y) * kWarps) {
-        const bool isq = r < P.n_q, isk = !isq && r < P.n_q + c.n_heads;
-        const int head = isq ? r : (isk ? r - P.n_q : r - P.n_q - c.n_heads);
-        const IO *src = static_cast<const IO *>(isq ? P.q : (isk ? P.k : P.v)) +
-                        tok * (isq ? P.ldq : (isk ? P.ldk : P.ldv)) + int64_t(head) * D;
-        float y[PASSES][N];
+    while (base < rows) {
+        if (!P.adjacent && half > 0) {
+            __syncwarp();
 #pragma unroll
-        for (int p = 0; p < PASSES; ++p) {
-            const int e = (p * 32 + lane) * N;
+            for (int i = 0; i < BATCH; ++i)
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                y[p][j] = 0.f;
-                if (e >= D)
-                    continue;
-                const float x = load1(src + e + j);
-                y[p][j] = x;
-                if ((isq || isk) && e + j < P.n_rot) {
-                    const bool second = P.adjacent ? (j & 1) : e + j >= half;
-                    const int pair = P.adjacent ? (e + j) >> 1 : (second ? e + j - half : e + j);
-                    const int at = P.adjacent ? (e + j) ^ 1 : (second ? e + j - half : e + j + half);
-                    const float2 w = turn[pair];
-                    const float a = __fmul_rn(x, w.x), b = __fmul_rn(load1(src + at), w.y);
-                    y[p][j] = second ? __fadd_rn(a, b) : __fsub_rn(a, b);
+                for (int p = 0; p < PASSES; ++p)
+                    staged[warp][i][p * 32 + lane] = x[i][p].raw;
+            __syncwarp();
+        }
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const int r = base + i * stride + sub;
+            const bool isq = r < P.n_q, isk = !isq && r < P.n_q + c.n_heads;
+            const IO *row = reinterpret_cast<const IO *>(staged[warp][i] + (lane - u));
+            const int head = isq ? r : (isk ? r - P.n_q : r - P.n_q - c.n_heads);
+#pragma unroll
+            for (int p = 0; p < PASSES; ++p) {
+                const int e = (p * 32 + u) * N;
+                const bool active = sub < rpw && r < rows && e < D;
+                float y[N];
+                x[i][p].values(y);
+                if (active && turned(r, e)) {
+                    float o[N];  // the partners
+                    if (P.adjacent) {
+#pragma unroll
+                        for (int j = 0; j < N; ++j)
+                            o[j] = y[j ^ 1];
+                    } else if (aligned) {
+                        Chunk<IO> other;
+                        other.load(row + (e < half ? e + half : e - half));
+                        other.values(o);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < N; ++j) {
+                            const int d = e + j;
+                            o[j] = load1(row + (d < half ? d + half : max(d - half, 0)));
+                        }
+                    }
+                    if (!P.adjacent && aligned) {
+                        const bool second = e >= half;
+                        const float sign = second ? 1.f : -1.f;
+                        const float4 *cs =
+                            reinterpret_cast<const float4 *>(turn + (second ? e - half : e));
+#pragma unroll
+                        for (int j = 0; j < N; j += 2) {
+                            const float4 w = cs[j / 2];
+                            y[j] = __fadd_rn(__fmul_rn(y[j], w.x), __fmul_rn(o[j], sign * w.y));
+                            y[j + 1] =
+                                __fadd_rn(__fmul_rn(y[j + 1], w.z), __fmul_rn(o[j + 1], sign * w.w));
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < N; ++j) {
+                            if (e + j >= P.n_rot)
+                                continue;
+                            const bool second = P.adjacent ? (j & 1) : e + j >= half;
+                            const float2 w =
+                                turn[P.adjacent ? (e + j) >> 1 : (second ? e + j - half : e + j)];
+                            const float b = __fmul_rn(o[j], w.y);
+                            const float a = __fmul_rn(y[j], w.x);
+                            y[j] = second ? __fadd_rn(a, b) : __fsub_rn(a, b);
+                        }
+                    }
                 }
+                if (isq && active)
+                    store_values<N>(static_cast<IO *>(P.q_out) + tok * P.ldqo + head * D + e, y);
+                // (Q8_0: all lanes shuffle where any of the warp's rows is not q's)
+                if (KIND == kQ8 ? base + i * stride + rpw > P.n_q : !isq)
+                    put<KIND, N>(c, isk, row0 + int64_t(head) * c.page_size, D, e, y,
+                                 active && !isq && row0 >= 0);
             }
         }
-        __syncwarp();  // q_out may be q: every load of the row is done before its first store
-#pragma unroll
-        for (int p = 0; p < PASSES; ++p) {
-            const int e = (p * 32 + lane) * N;
-            if (isq) {
-                if (e < D)
-                    store_values<N>(static_cast<IO *>(P.q_out) + tok * P.ldqo + int64_t(head) * D +
-                                        e, y[p]);
-            } else {
-                put<KIND, N>(c, isk, row0 + int64_t(head) * c.page_size, D, e, y[p],
-                             e < D && row0 >= 0);
-            }
-        }
+        base += BATCH * stride;
+        if (base < rows)
+            load(base);
     }
 }
 
@@ -497,12 +566,15 @@ cudaError_t append_for_dim(const AppendArgs &a, int sm_count, cudaStream_t s)
     const bool regular = append_regular<KIND, N>(a);
     // Few tokens: a block takes as few heads as keep about four blocks on
     // every SM; from there on a block takes the whole token.
-    const int rows = kWarps * (regular ? 32 / (a.c.D / N / 2) : 1);  // of a block at a time
+    // rows of a block at a time
+    const int rows = kWarps * (regular ? 32 / (a.c.D / N / 2) : std::max(1, 32 / (a.c.D / N)));
     const int passes = (a.n_q + 2 * a.c.n_heads + rows - 1) / rows;
     const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(passes, 4 * sm_count / a.T));
     const dim3 grid(unsigned(a.T), unsigned(parts));
     if (!regular)
-        return launch(append_any_kernel<KIND, IO>, grid, kThreads, s, a);
+        return launch(N == 4 && a.c.D > 128 ? append_any_kernel<KIND, IO, N == 4 ? 2 : 1>
+                                            : append_any_kernel<KIND, IO, 1>,
+                      grid, kThreads, s, a);
     switch (a.c.D) {
     case 64: return launch(append_kernel<KIND, IO, 64>, grid, kThreads, s, a);
     case 96: return launch(append_kernel<KIND, IO, 96>, grid, kThreads, s, a);

@@ -136,6 +136,20 @@ def test_queries_rotated_in_place(io, D, pairing):
     run("bf16", 40, 2, 4, D, 16, io=io, pairing=pairing, in_place=True)
 
 
+@pytest.mark.parametrize("kind", ["f16", "q8_0"])
+@pytest.mark.parametrize("io", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("D,n_rot", [(64, 32), (96, 96), (96, 36), (128, 64), (128, 100), (192, 96),
+                                     (192, 184), (256, 64), (256, 254)])
+@pytest.mark.parametrize("heads,group,in_place", [(1, 1, True), (3, 5, True), (2, 8, False)])
+def test_partial_rotation_of_every_type(kind, io, D, n_rot, heads, group, in_place):
+    run(kind, 12, heads, group, D, 16, io=io, n_rot=n_rot, in_place=in_place, seed=D + n_rot)
+
+
+@pytest.mark.parametrize("n_rot,pairing", [(64, "halves"), (24, "halves"), (20, "adjacent")])
+def test_whole_tokens_of_partial_rotation(n_rot, pairing):
+    run("q8_0", 700, 3, 7, 96, 16, io="bf16", n_rot=n_rot, pairing=pairing, in_place=True)
+
+
 def test_large_positions():
     run("bf16", 30, 1, 2, 64, 16, top=2 ** 31 - 1, seed=3)
     run("bf16", 30, 1, 2, 64, 16, top=200000, seed=4)
