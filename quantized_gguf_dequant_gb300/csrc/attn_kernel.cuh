@@ -415,10 +415,14 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
         per = share(total, __reduce_max_sync(0xffffffffu, sp.n));
         // With fewer items than blocks, shares a little larger may let every
         // block keep to one item: a second one costs it another start and join.
+        // (Sixteenths: Q8_0's wide rows take too long for their bytes to wait for
+        // a larger share; 16 sequences of 4096 keys: 32 us, with larger ones 34,
+        // head_dim 256: 54 and 60.)
+        constexpr unsigned MORE = KIND == kQ8 && D >= 128 && WARPS == 4 ? 0 : 4;
         unsigned stride = own;
         if (per < (1 << 23) && __reduce_max_sync(0xffffffffu, own) < (1u << 23)) {
             const unsigned p0 = unsigned(per);
-            for (unsigned more = 0; more <= 4; more += 2) {
+            for (unsigned more = 0; more <= MORE; more += 2) {
                 const unsigned p = p0 + p0 * more / 16u;
                 unsigned parts = unsigned(__fdividef(float(own), float(p)));
                 parts += parts * p < own;  // (rounded down or exact: up)
@@ -1451,16 +1455,17 @@ cudaError_t launch_warps(AttnParams &p, int sm_count, cudaStream_t s)
 }
 
 // Warps of a block.  Narrow rows: eight, two blocks on an SM (24 sequences of
-// 1024 keys, head_dim 64: 16.7 us, with four warps 20).  16-bit rows of 128: four,
-// three blocks, which overlap one another's starts and joins; with few items, whose
+// 1024 keys, head_dim 64: 16.2 us, with four warps 20).  Rows of 128: four, three
+// blocks, which overlap one another's starts and joins; with few items, whose
 // parts all have to be joined, one block of twelve (one sequence of 131071 keys:
-// 50.5 us, with four 53.5; 337 keys: 7.0 us, with four 8.0).
+// 50.3 us, with four 53.5; 337 keys: 6.9 us, with four 8.0; Q8_0, four sequences of
+// 8000 keys: 14.4 us, with four 20.6).
 template <Kind KIND, int D, int HEADS>
 cudaError_t launch_heads(AttnParams &p, int sm_count, cudaStream_t s)
 {
     if constexpr (KIND != kQ8 && D == 64)
         return launch_warps<KIND, D, HEADS, 8>(p, sm_count, s);
-    if constexpr (KIND != kQ8 && D == 128 && HEADS <= 8) {
+    if constexpr (D == 128 && HEADS <= 8) {
         const int64_t items =
             int64_t(p.a.n_seqs) * p.a.c.n_heads * ((p.group + HEADS - 1) / HEADS);
         if (items * 4 <= sm_count)
