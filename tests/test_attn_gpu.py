@@ -130,6 +130,16 @@ def test_counts_of_sequences(kind, B, longest):
     check(kind, lens, 1, 4, 64, 16, seed=B)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D,group,page", [(128, 4, 16), (128, 8, 16), (128, 3, 24), (128, 16, 16),
+                                          (256, 4, 16), (96, 7, 16)])
+def test_batches_of_wide_rows(kind, D, group, page):
+    rng = np.random.default_rng(D + group)
+    lens = [int(n) for n in rng.integers(0, 120, 24)]
+    lens[3], lens[11], lens[23] = 1900, 0, 1025
+    check(kind, lens, 3, group, D, page, seed=D)
+
+
 def test_many_sequences_all_empty_but_the_last():
     check("f16", [0] * 99 + [17], 2, 2, 64, 16)
     check("f16", [0] * 77, 2, 2, 64, 16)
