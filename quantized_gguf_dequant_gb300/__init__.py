@@ -404,6 +404,7 @@ class Rope:
         if inv_freq.dtype != torch.float32 or not inv_freq.is_cuda or not inv_freq.is_contiguous():
             raise ValueError("inv_freq must be a contiguous float32 tensor on the CUDA device")
         self.inv_freq = inv_freq  # keep the device memory alive
+        self.device = inv_freq.device.index
         self.desc = RopeDesc(2 * n, int(pairing == "adjacent"), len(sections),
                              (ctypes.c_int32 * 4)(*sections), inv_freq.data_ptr())
         self.address = ctypes.addressof(self.desc)
@@ -412,8 +413,8 @@ class Rope:
 class KVCache:
     """A paged key-value cache on the device (qmm_kv_create) with the calls
     that use it.  kind: F16, BF16 or Q8_0.  k, v: its two buffers (any dtype,
-    at least kv_bytes() bytes each); made and zeroed here when not given.
-    Every call takes a stream (a torch stream or a raw handle; default: the
+    at least kv_bytes() bytes each, on the current device); made and zeroed here
+    when not given.  Every call takes a stream (a torch stream or a raw handle; default: the
     current one)."""
 
     def __init__(self, kind: int, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int,
@@ -430,13 +431,17 @@ class KVCache:
             if t.numel() * t.element_size() < need:
                 raise ValueError(f"the {name} buffer holds {t.numel() * t.element_size()} bytes; "
                                  f"{need} are needed")
+            # the handle belongs to the current device, and so do its calls
+            if not t.is_cuda or t.device.index != torch.cuda.current_device():
+                raise ValueError(f"the {name} buffer lives on {t.device}, but device "
+                                 f"{torch.cuda.current_device()} is current")
         self.k, self.v = k, v  # keep the buffers alive as long as the handle
         self._native = native()
         h = ctypes.c_void_p()
         _check(lib().qmm_kv_create(kind, n_pages, page_size, n_kv_heads, head_dim, _ptr(k),
                                    _ptr(v), ctypes.byref(h)))
         self.h = h.value
-        self._cache = self._native.cache(self.h, k.device.index or 0, n_kv_heads, head_dim)
+        self._cache = self._native.cache(self.h, k.device.index, n_kv_heads, head_dim)
 
     def close(self):
         if getattr(self, "h", None):
@@ -485,7 +490,7 @@ def logits_adjust(logits, out=None, *, history=None, history_offsets=None, repea
                   presence=None, frequency=None, bias_ids=None, bias_values=None,
                   bias_offsets=None, mask=None, stream=None):
     """qmm_logits_adjust: penalties, biases and a mask on [rows, vocabulary] (or
-    one row of) logits.  history, bias_ids: int32, ragged by the rows + 1 int64
+    one row of) logits on the current device.  history, bias_ids: int32, ragged by the rows + 1 int64
     offsets; repeat, presence, frequency: float32 [rows]; mask: int32 words
     [rows, words], or one row [words] for all.  out may be logits."""
     return (_native or native()).logits(logits, out, history, history_offsets, repeat, presence,

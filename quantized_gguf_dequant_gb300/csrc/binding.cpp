@@ -9,6 +9,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -245,7 +246,18 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n)
             return nullptr;
         rope = static_cast<const qmm_rope *>(PyLong_AsVoidPtr(at));
         Py_DECREF(at);
-        if (!rope || !flat(a[5], "pos", at::kInt, rope->n_axes * T, c->device, pp))
+        if (!rope || !(at = PyObject_GetAttrString(a[6], "device")))
+            return nullptr;
+        const long device = PyLong_AsLong(at);
+        Py_DECREF(at);
+        if (PyErr_Occurred())
+            return nullptr;
+        if (device != c->device) {
+            PyErr_Format(PyExc_ValueError, "rope's inv_freq lives on device %ld, the call is for "
+                         "device %d", device, c->device);
+            return nullptr;
+        }
+        if (!flat(a[5], "pos", at::kInt, rope->n_axes * T, c->device, pp))
             return nullptr;
     }
     qmm_status rc;
@@ -401,6 +413,14 @@ PyObject *logits(PyObject *, PyObject *const *a, Py_ssize_t n)
         return nullptr;
     }
     const int device = z->device().index();
+    // The C entry launches on the current device, whatever the pointers say.
+    // (A cache's calls are held to its device by the entry.)
+    c10::DeviceIndex current = -1;
+    if (c10::cuda::GetDevice(&current) != cudaSuccess || device != current) {
+        PyErr_Format(PyExc_ValueError, "logits live on device %d, but device %d is current", device,
+                     int(current));
+        return nullptr;
+    }
     const int64_t B = shape.size() == 2 ? shape[0] : 1, V = shape.back();
     int64_t ld = V, ldo = V;
     if (B > 1)
