@@ -456,7 +456,7 @@ class KVCache:
 
     def append(self, k, v, slots, q=None, pos=None, rope=None, q_out=None, stream=None):
         """qmm_kv_append: rotate q and k ([T, heads, head_dim]) and store k and
-        v at slots ([T] int64).  pos: [n_axes, T] (or [T]) int32.  Returns the
+        v at slots ([T] int64).  pos: [n_axes, T] int32 (one axis: [T] will do).  Returns the
         rotated q (into q_out, which may be q), or None without q."""
         return self._native.append(self._cache, k, v, slots, q, pos, rope, q_out, stream)
 

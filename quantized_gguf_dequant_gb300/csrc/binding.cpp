@@ -259,6 +259,15 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n)
         }
         if (!flat(a[5], "pos", at::kInt, rope->n_axes * T, c->device, pp))
             return nullptr;
+        // [T, axes] has as many elements and would turn tokens by others' positions
+        if (pp && rope->n_axes > 1) {
+            const at::IntArrayRef s = THPVariable_Unpack(a[5]).sizes();
+            if (s.size() != 2 || s[0] != rope->n_axes || s[1] != T) {
+                PyErr_Format(PyExc_ValueError, "pos has shape %s; (%d, %lld) is needed",
+                             shape_of(s).c_str(), int(rope->n_axes), (long long)T);
+                return nullptr;
+            }
+        }
     }
     qmm_status rc;
     Py_BEGIN_ALLOW_THREADS

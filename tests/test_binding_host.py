@@ -73,3 +73,17 @@ def test_frequencies_of_another_device_refuse(outcome):
     assert outcome("append", **new_tokens(0, 0)) == "called"
     got = outcome("append", **new_tokens(0, 1))
     assert got.startswith("ValueError") and "inv_freq" in got
+
+
+@pytest.mark.parametrize("pairs,shape,taken", [
+    ([16, 16], [2, 3], True), ([16, 16], [3, 2], False), ([16, 16], [6], False),
+    ([10, 11, 11], [3, 3], True), ([32], [3], True), ([32], [1, 3], True), ([32], [4], False),
+    ([32], [2, 3], False)])
+def test_positions_are_taken_by_axis_then_token(outcome, pairs, shape, taken):
+    args = new_tokens(0, 0)
+    args["rope"]["pairs"], args["pos"] = pairs, [shape, "i32", 0]
+    got = outcome("append", **args)
+    if taken:
+        assert got == "called"
+    else:
+        assert got.startswith("ValueError") and "pos" in got
