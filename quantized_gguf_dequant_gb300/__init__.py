@@ -414,8 +414,11 @@ class KVCache:
     """A paged key-value cache on the device (qmm_kv_create) with the calls
     that use it.  kind: F16, BF16 or Q8_0.  k, v: its two buffers (any dtype,
     at least kv_bytes() bytes each, on the current device); made and zeroed here
-    when not given.  Every call takes a stream (a torch stream or a raw handle; default: the
-    current one)."""
+    when not given.  Every call takes a stream (a torch stream or a raw handle;
+    default: the current one).  Calls on one cache share its workspace and must
+    be ordered, as on one stream.  On another stream than the current one a call waits for
+    nothing: its inputs must be ready there (stream.wait_stream), but may be
+    dropped at once."""
 
     def __init__(self, kind: int, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int,
                  k=None, v=None):
@@ -492,7 +495,8 @@ def logits_adjust(logits, out=None, *, history=None, history_offsets=None, repea
     """qmm_logits_adjust: penalties, biases and a mask on [rows, vocabulary] (or
     one row of) logits on the current device.  history, bias_ids: int32, ragged by the rows + 1 int64
     offsets; repeat, presence, frequency: float32 [rows]; mask: int32 words
-    [rows, words], or one row [words] for all.  out may be logits."""
+    [rows, words], or one row [words] for all.  out may be logits.  stream: as
+    for a KVCache's calls."""
     return (_native or native()).logits(logits, out, history, history_offsets, repeat, presence,
                                         frequency, bias_ids, bias_values, bias_offsets, mask,
                                         stream)

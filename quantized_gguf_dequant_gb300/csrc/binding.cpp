@@ -164,6 +164,22 @@ PyObject *output(at::IntArrayRef shape, at::ScalarType type, int device, void *s
     return THPVariable_Wrap(std::move(t));
 }
 
+// What a call on a stream that is not the current one reads or writes: memory
+// that the caller drops is not given out again before that stream is done.
+// named: the call's stream argument.
+void used_on(PyObject *named, void *stream, int device, std::initializer_list<PyObject *> given)
+{
+    if (named == Py_None ||
+        c10::cuda::getCurrentCUDAStream(c10::DeviceIndex(device)).stream() == stream)
+        return;
+    const c10::Stream on = c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream),
+                                                            c10::DeviceIndex(device))
+                               .unwrap();
+    for (PyObject *o : given)
+        if (o && THPVariable_Check(o) && THPVariable_Unpack(o).numel() > 0)
+            THPVariable_Unpack(o).record_stream(on);
+}
+
 bool ok(qmm_status rc)
 {
     if (rc == QMM_OK)
@@ -240,6 +256,7 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n)
         }
     }
     const qmm_rope *rope = nullptr;
+    Held inv_freq;
     if (a[6] != Py_None) {
         PyObject *at = PyObject_GetAttrString(a[6], "address");
         if (!at)
@@ -257,6 +274,8 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n)
                          "device %d", device, c->device);
             return nullptr;
         }
+        if (a[8] != Py_None && !(inv_freq.o = PyObject_GetAttrString(a[6], "inv_freq")))
+            return nullptr;
         if (!flat(a[5], "pos", at::kInt, rope->n_axes * T, c->device, pp))
             return nullptr;
         // [T, axes] has as many elements and would turn tokens by others' positions
@@ -276,6 +295,7 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n)
     Py_END_ALLOW_THREADS
     if (!ok(rc))
         return nullptr;
+    used_on(a[8], stream, c->device, {a[1], a[2], a[3], a[4], a[5], a[7], inv_freq.o});
     if (out.o)
         return out.release();
     Py_RETURN_NONE;
@@ -347,6 +367,7 @@ PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t n)
     Py_END_ALLOW_THREADS
     if (!ok(rc))
         return nullptr;
+    used_on(a[11], stream, c->device, {a[1], a[2], a[3], a[7], a[8], a[9]});
     return want ? PyTuple_Pack(2, out.o, lse.o) : out.release();
     END_HANDLE_TH_ERRORS
 }
@@ -396,7 +417,10 @@ PyObject *read(PyObject *, PyObject *const *a, Py_ssize_t n)
     rc = g_read(c->handle, id, T, static_cast<const int64_t *>(sp), p[0], ld[0], p[1], ld[1],
                 stream);
     Py_END_ALLOW_THREADS
-    return ok(rc) ? PyTuple_Pack(2, out[0].o, out[1].o) : nullptr;
+    if (!ok(rc))
+        return nullptr;
+    used_on(a[5], stream, c->device, {a[1], a[3], a[4]});
+    return PyTuple_Pack(2, out[0].o, out[1].o);
     END_HANDLE_TH_ERRORS
 }
 
@@ -502,7 +526,10 @@ PyObject *logits(PyObject *, PyObject *const *a, Py_ssize_t n)
     Py_BEGIN_ALLOW_THREADS
     rc = g_logits(id, B, V, zp, ld, &r, op, ldo, stream);
     Py_END_ALLOW_THREADS
-    return ok(rc) ? out.release() : nullptr;
+    if (!ok(rc))
+        return nullptr;
+    used_on(a[11], stream, device, {a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8], a[9], a[10]});
+    return out.release();
     END_HANDLE_TH_ERRORS
 }
 

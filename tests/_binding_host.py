@@ -1,7 +1,7 @@
 """The native binding (csrc/binding.cpp) driven without a GPU: tensors over
 host memory that claim a CUDA device, C entries replaced by functions that note
 the call, and a runtime whose current device is 0.  Runs as a child process
-(the stand-in for cudaGetDevice is preloaded): reads a list of calls as JSON,
+(the stand-ins for what it asks the runtime are preloaded): reads a list of calls as JSON,
 prints what became of each: "called" or the refusal."""
 from __future__ import annotations
 
@@ -28,7 +28,9 @@ def build(directory: str) -> None:
          "-ltorch_python", "-ltorch_cpu", "-lc10"], check=True, capture_output=True)
     source = os.path.join(directory, "device.c")
     with open(source, "w") as f:
-        f.write("int cudaGetDevice(int *d) { *d = 0; return 0; }\n")
+        f.write("int cudaGetDevice(int *d) { *d = 0; return 0; }\n"
+                "int cudaGetDeviceCount(int *n) { *n = 2; return 0; }\n"
+                "int cudaDeviceGetStreamPriorityRange(int *a, int *b) { *a = *b = 0; return 0; }\n")
     subprocess.run(["gcc", "-shared", "-fPIC", source, "-o", os.path.join(directory, "device.so")],
                    check=True, capture_output=True)
 
