@@ -473,7 +473,8 @@ class KVCache:
                                    out, lse, return_lse, stream)
 
     def read(self, slots, dtype=None, k_out=None, v_out=None, stream=None):
-        """qmm_kv_read: (k, v) values of the slots, [T, n_kv_heads, head_dim]."""
+        """qmm_kv_read: (k, v) values of the slots, [T, n_kv_heads, head_dim], in
+        dtype (default: that of the output that is given, else float32)."""
         return self._native.read(self._cache, slots, dtype, k_out, v_out, stream)
 
     def status(self) -> int:

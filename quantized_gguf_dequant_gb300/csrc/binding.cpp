@@ -389,8 +389,10 @@ PyObject *read(PyObject *, PyObject *const *a, Py_ssize_t n)
             return nullptr;
         }
         type = reinterpret_cast<THPDtype *>(a[2])->scalar_type;
-    } else if (a[3] != Py_None && THPVariable_Check(a[3])) {
+    } else if (THPVariable_Check(a[3])) {
         type = THPVariable_Unpack(a[3]).scalar_type();
+    } else if (THPVariable_Check(a[4])) {
+        type = THPVariable_Unpack(a[4]).scalar_type();
     }
     const int64_t T = slots->numel();
     int id;
