@@ -20,8 +20,8 @@
 //
 // Measured on one GB300 (bytes of keys, values, q and out; the card copies
 // 6.77 TB/s): 16 sequences of 2000-4001 keys, 32 heads on 8 of 128, bf16: 32.7 us,
-// 5.0 TB/s; 64 sequences of 8192-16384 keys in Q8_0: 276 us, 6.0 TB/s (bound by
-// issuing instructions: 460 a 16 keys); one of 131071 keys, 32 heads on 4, f16,
+// 5.0 TB/s; 64 sequences of 8192-16384 keys in Q8_0: 284 us, 5.8 TB/s (bound by
+// issuing instructions: about 490 a 16 keys); one of 131071 keys, 32 heads on 4, f16,
 // capped: 50 us, 5.3 TB/s; 24 with windows of 1024, 12 heads of 64: 16.3 us,
 // 4.3 TB/s; one of 337 keys: 6.8 us.  Of the 32.7 us the loads take about 22, at the
 // card's rate; 2.3 go by until the first tile is asked for (lengths, page ids,
@@ -50,11 +50,13 @@
 // stand.  The value product of a tile starts from zero and is added to the
 // running sum with a rounding FMA: sums kept inside the tensor cores lose
 // low bits over thousands of tiles.
-// Q8_0: key codes + 128 enter as f16 subnormals (one byte permute; the 128s'
-// part is where the sum starts from), value codes as f16 integers; key scales
-// multiply the scores of their 32-value block, value scales the
-// probabilities, which are first brought to f16's range by the power of two
-// that the largest value scale so far asks for.
+// Q8_0: codes enter as f16 integers; key scales multiply the scores of their
+// 32-value block, value scales the probabilities, which are first brought to
+// f16's range by the power of two that the largest value scale so far asks for.
+// (Codes + 128 as f16 subnormals are a byte permute cheaper a pair, but then the
+// sums carry 128 times the sum of q: with one large code a block and small ones
+// beside it scores were off by 12 units of 2^-24 sum |q k| instead of 0.2.  The
+// exact codes cost 3 to 4 %: 64 sequences 284 us instead of 277.)
 #pragma once
 
 #include <algorithm>
@@ -256,12 +258,6 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
 template <Kind KIND>
 using Half = typename std::conditional<KIND == kBF16, __nv_bfloat16, __half>::type;
 
-// Two of four bytes u as f16 subnormals u * 2^-24 (exact operands).
-__device__ __forceinline__ uint32_t bytes_f16(uint32_t u, unsigned sel)
-{
-    return __byte_perm(u, 0u, sel);
-}
-
 // Four int8 codes, as bytes code + 128, to two pairs of f16: 1024 + byte by
 // the exponent byte 0x64, minus 1152.
 __device__ __forceinline__ uint32_t codes_f16(uint32_t biased, unsigned sel)
@@ -355,7 +351,6 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
     __shared__ unsigned valid_ring[kWarps][STAGES];
     __shared__ int qexp[HEADS];
     __shared__ bool qfinite[HEADS];
-    __shared__ float q_off[HEADS][D / 32];
     __shared__ bool last_block;
 
     const AttnArgs &A = P.a;
@@ -824,7 +819,6 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
                 uint16_t *frag3 =
                     reinterpret_cast<uint16_t *>(smem + hh * S::QF1 + S::KSTEPS * 512);
                 const float f = exp2i(e);
-                float off[D / 32] = {};
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
                     const int d = i * 16 + lt;
@@ -848,7 +842,6 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
                     const H p0 = H(x);
                     const float r1 = x - float(p0);
                     const H p1 = H(r1);
-                    off[i / 2] += float(p0) + float(p1);
                     const int hr = h & 7;  // the head's row of its operand
                     put(hr, p0);
                     put(hr + NH, p1);
@@ -861,32 +854,17 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
                             *reinterpret_cast<const uint16_t *>(&p2);
                     }
                 }
-                if constexpr (KIND == kQ8) {  // -128 * 2^-24 times each block's sum of q
-#pragma unroll
-                    for (int blk = 0; blk < D / 32; ++blk) {
-#pragma unroll
-                        for (int o = 1; o < 16; o <<= 1)
-                            off[blk] += __shfl_xor_sync(0xffffffffu, off[blk], o);
-                        if (lt == 0)
-                            q_off[h][blk] = off[blk] * -0x1p-17f;
-                    }
-                }
             }
         }
         __syncthreads();
 
         const int hg = g & (NH - 1);  // the head of an operand whose scores this lane holds
-        float qscale[HT], slope[HT], qoff[HT][D / 32];
+        float qscale[HT], slope[HT];
 #pragma unroll
         for (int hh = 0; hh < HT; ++hh) {
             const int hd = hh * 8 + hg;
-            qscale[hh] = A.scale * exp2i(-qexp[hd]) * (KIND == kQ8 ? 0x1p24f : 1.f);
+            qscale[hh] = A.scale * exp2i(-qexp[hd]);
             slope[hh] = A.alibi && hd < nh ? __ldg(A.alibi + head0 + hd) * kLog2e : 0.f;
-            if constexpr (KIND == kQ8) {
-#pragma unroll
-                for (int blk = 0; blk < D / 32; ++blk)
-                    qoff[hh][blk] = g < NH ? q_off[hd][blk] : 0.f;
-            }
         }
         const float cap_inv = A.softcap > 0.f ? 1.f / A.softcap : 0.f;
         // f16 probabilities are carried 2^14 times as large, clear of its subnormals
@@ -928,8 +906,6 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
                     }
 #pragma unroll
                 for (int blk = 0; blk < D / 32; ++blk) {
-                    // codes + 128 as subnormals; the 128s' part of the sum, which
-                    // is q's, is where it starts from
                     uint4 a[2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -947,15 +923,15 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
                     for (int u = 0; u < KT; ++u)
 #pragma unroll
                         for (int n = 0; n < 2; ++n) {
-                            float c[4] = {qoff[hh][blk], qoff[hh][blk], 0.f, 0.f};
+                            float c[4] = {};
                             uint2 w = lds64(
                                 S::column(kb + (u * kGroup + n * 8) * S::RS + key_row, blk));
                             w.x ^= 0x80808080u;
                             w.y ^= 0x80808080u;
-                            mma<KIND>(c, a[0].x, a[0].y, a[0].z, a[0].w, bytes_f16(w.x, 0x4140),
-                                      bytes_f16(w.x, 0x4342));
-                            mma<KIND>(c, a[1].x, a[1].y, a[1].z, a[1].w, bytes_f16(w.y, 0x4140),
-                                      bytes_f16(w.y, 0x4342));
+                            mma<KIND>(c, a[0].x, a[0].y, a[0].z, a[0].w, codes_f16(w.x, 0x4140),
+                                      codes_f16(w.x, 0x4342));
+                            mma<KIND>(c, a[1].x, a[1].y, a[1].z, a[1].w, codes_f16(w.y, 0x4140),
+                                      codes_f16(w.y, 0x4342));
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
                                 const float2 sc = unpack2(ksc[u][2 * n + y][blk / 2], __half());
@@ -1027,7 +1003,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
                         for (int d = 0; d < D; ++d)
                             dot += load_any(A.q, q0 + d, A.dtype) *
                                    value_at<KIND, D>(C.k, C.ks, row, d);
-                        s[u][x] = dot * exp2i(qexp[hd]) * (KIND == kQ8 ? 0x1p-24f : 1.f);
+                        s[u][x] = dot * exp2i(qexp[hd]);
                     }
             }
             // scores in base 2
