@@ -20,7 +20,7 @@
 //
 // Measured on one GB300 (bytes of keys, values, q and out; the card copies
 // 6.77 TB/s): 16 sequences of 2000-4001 keys, 32 heads on 8 of 128, bf16: 32.7 us,
-// 5.0 TB/s; 64 sequences of 8192-16384 keys in Q8_0: 284 us, 5.8 TB/s (bound by
+// 5.0 TB/s; 64 sequences of 8192-16384 keys in Q8_0: 287 us, 5.7 TB/s (bound by
 // issuing instructions: about 490 a 16 keys); one of 131071 keys, 32 heads on 4, f16,
 // capped: 50 us, 5.3 TB/s; 24 with windows of 1024, 12 heads of 64: 16.3 us,
 // 4.3 TB/s; one of 337 keys: 6.8 us.  Of the 32.7 us the loads take about 22, at the
@@ -52,11 +52,11 @@
 // low bits over thousands of tiles.
 // Q8_0: codes enter as f16 integers; key scales multiply the scores of their
 // 32-value block, value scales the probabilities, which are first brought to
-// f16's range by the power of two that the largest value scale so far asks for.
-// (Codes + 128 as f16 subnormals are a byte permute cheaper a pair, but then the
-// sums carry 128 times the sum of q: with one large code a block and small ones
-// beside it scores were off by 12 units of 2^-24 sum |q k| instead of 0.2.  The
-// exact codes cost 3 to 4 %: 64 sequences 284 us instead of 277.)
+// f16's range by the power of two that the largest finite value scale so far
+// asks for.  (Codes + 128 as f16 subnormals are a byte permute cheaper a pair,
+// but then the sums carry 128 times the sum of q: with one large code a block
+// and small ones beside it scores were off by 12 units of 2^-24 sum |q k| instead
+// of 0.2.  That and the look for infinite scales cost the 64 sequences 277 -> 287 us.)
 #pragma once
 
 #include <algorithm>
@@ -211,6 +211,12 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr)
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
 }
+__device__ __forceinline__ uint32_t lds16(uint32_t addr)
+{
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+    return v;
+}
 // N words from a 4-byte boundary (one load where N is 1, 2 or 4 and the
 // address a multiple of their size).
 template <int N>
@@ -267,6 +273,17 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t biased, unsigned sel)
                               __half2half2(__ushort_as_half(0x6480)));
     return *reinterpret_cast<const uint32_t *>(&h);
 }
+
+// Codes 0 and 2 of four int8 codes as two f16: 1024 + (code + 128) in one logical
+// operation, minus 1152; and codes 1 and 3.
+__device__ __forceinline__ uint32_t even_codes(uint32_t w)
+{
+    const uint32_t x = (w & 0x00ff00ffu) ^ 0x64806480u;
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&x),
+                              __half2half2(__ushort_as_half(0x6480)));
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t odd_codes(uint32_t w) { return even_codes(w >> 8); }
 
 // The tile list of one sequence: keys [lo, hi), tiles t0 .. t0 + n - 1 (tiles
 // counted from key 0).
@@ -822,20 +839,23 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
                     const int d = i * 16 + lt;
-                    int ks, tt, hi;
+                    int ks, tt, hi, lo;
                     if constexpr (KIND == kQ8) {
-                        // lane t of a key holds codes 8t .. 8t+7 of a 32-block
+                        // lane t of a key holds codes 8t .. 8t+7 of a 32-block, in each
+                        // four of them the even ones first
                         ks = (d >> 5) * 2 + ((d >> 2) & 1);
                         tt = (d & 31) >> 3;
-                        hi = (d >> 1) & 1;
+                        hi = d & 1;
+                        lo = (d >> 1) & 1;
                     } else {
                         ks = d >> 4;
                         tt = (d & 7) >> 1;
                         hi = (d >> 3) & 1;
+                        lo = d & 1;
                     }
                     // row r of the operand: lane 4 (r % 8) + tt, register 2 hi + r / 8
                     auto put = [&](int r, H v) {
-                        frag[(ks * 32 + (r & 7) * 4 + tt) * 8 + (2 * hi + (r >> 3)) * 2 + (d & 1)] =
+                        frag[(ks * 32 + (r & 7) * 4 + tt) * 8 + (2 * hi + (r >> 3)) * 2 + lo] =
                             *reinterpret_cast<const uint16_t *>(&v);
                     };
                     const float x = qv[hh][i] * f;
@@ -850,7 +870,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
                         put(hr + 12, H(0.f));
                     } else if constexpr (S::THIRD) {
                         const H p2 = H(r1 - float(p1));
-                        frag3[(ks * 32 + hr * 4 + tt) * 4 + hi * 2 + (d & 1)] =
+                        frag3[(ks * 32 + hr * 4 + tt) * 4 + hi * 2 + lo] =
                             *reinterpret_cast<const uint16_t *>(&p2);
                     }
                 }
@@ -926,12 +946,8 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
                             float c[4] = {};
                             uint2 w = lds64(
                                 S::column(kb + (u * kGroup + n * 8) * S::RS + key_row, blk));
-                            w.x ^= 0x80808080u;
-                            w.y ^= 0x80808080u;
-                            mma<KIND>(c, a[0].x, a[0].y, a[0].z, a[0].w, codes_f16(w.x, 0x4140),
-                                      codes_f16(w.x, 0x4342));
-                            mma<KIND>(c, a[1].x, a[1].y, a[1].z, a[1].w, codes_f16(w.y, 0x4140),
-                                      codes_f16(w.y, 0x4342));
+                            mma<KIND>(c, a[0].x, a[0].y, a[0].z, a[0].w, even_codes(w.x), odd_codes(w.x));
+                            mma<KIND>(c, a[1].x, a[1].y, a[1].z, a[1].w, even_codes(w.y), odd_codes(w.y));
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
                                 const float2 sc = unpack2(ksc[u][2 * n + y][blk / 2], __half());
@@ -1071,9 +1087,18 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
                 float dm = __half2float(__hmax(__low2half(mx), __high2half(mx)));
                 dm = fmaxf(dm, __shfl_xor_sync(0xffffffffu, dm, 1));
                 dm = fmaxf(dm, __shfl_xor_sync(0xffffffffu, dm, 2));
-                int ve = max(vexp[hh], int(__float_as_uint(dm) >> 23) - 127);
-                if (ve > 15)  // an infinite scale: the others keep theirs
-                    ve = vexp[hh] > -126 ? vexp[hh] : 15;
+                if (__any_sync(0xffffffffu, dm > FLT_MAX)) {  // an infinite scale: the largest of the others
+                    unsigned most = 0;
+#pragma unroll 1
+                    for (int i = lane; i < TILE * S::SP; i += 32) {
+                        const unsigned d = lds16(vsb + 2 * i) & 0x7fffu;
+                        if (d < 0x7c00u && (D % 64 == 0 || i % S::SP < D / 32))
+                            most = max(most, d);
+                    }
+                    most = __reduce_max_sync(0xffffffffu, most);
+                    dm = __half2float(__ushort_as_half(uint16_t(most)));
+                }
+                const int ve = max(vexp[hh], int(__float_as_uint(dm) >> 23) - 127);
                 const float fe = exp2i(max(-126, vexp[hh] - ve));
                 f0 *= fe;
                 f1 *= fe;

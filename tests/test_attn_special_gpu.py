@@ -1,0 +1,56 @@
+"""Infinities where the decode attention's formula still has an answer."""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import pytest
+
+from tests import _decode_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+q = pytest.importorskip("quantized_gguf_dequant_gb300")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("group", [4, 8])
+@pytest.mark.parametrize("before,beside,where", [
+    (1e-3, 100.0, 901), (1e-3, 60000.0, 901), (1e-6, 1.0, 901), (2.0, 3.0, 901), (1e-6, 1e-6, 901),
+    (1e-6, 1e-6, 3), (1e-3, 2.0, 3), (0.0, 1.0, 3)])
+def test_infinite_value_scale_beside_large_ones(D, group, before, beside, where):
+    """One block of one key's value has an infinite scale.  The other blocks'
+    outputs are what they are without it, also where the keys next to it have
+    larger scales than any before."""
+    rng = np.random.default_rng(D + group)
+    n, B = 1000, 160  # (enough items for a warp to take several tiles of each)
+    table, n_pages, slots = ref.table_for([n], 16, rng)
+    pages = ref.Pages(q, "q8_0", n_pages, 16, 1, D, rng)
+    codes, scales = pages.raw[1]
+    at = [(s // 16, 0, s % 16) for s in slots[0]]
+    for j, key in enumerate(at):
+        scales[key][:D // 32] = np.float16(before if j < 896 else beside)
+    scales[at[where]][1] = np.inf
+    with np.errstate(invalid="ignore"):
+        pages.val[1] = codes.astype(np.float64) * np.repeat(
+            scales[..., :D // 32].astype(np.float64), 32, axis=-1)
+    cache = pages.to_device(slots[0])
+    x = rng.standard_normal((B, group, D)).astype(np.float32)
+    scale = float(np.float32(1 / math.sqrt(D)))
+    got = cache.attend(torch.from_numpy(x).cuda(), torch.from_numpy(table).cuda().repeat(B, 1),
+                       torch.full((B,), n, dtype=torch.int32, device="cuda"), scale=scale)
+    got = got.double().cpu().numpy()
+    k, v = pages.rows(0, slots[0]), pages.rows(1, slots[0])
+    hit = np.zeros(D, bool)
+    hit[32:64] = True
+    plain = np.where(hit, 0.0, v)
+    for b in range(0, B, 40):
+        with np.errstate(invalid="ignore"):
+            want, _, _ = ref.attention(x[b].astype(np.float64), k, v, scale)
+        _, _, size = ref.attention(x[b].astype(np.float64), k, plain, scale)
+        tol, _ = ref.attention_bound(size, D)
+        assert (np.abs(got[b] - want)[:, ~hit] <= tol[:, None]).all()
+        # infinite, or NaN for code 0
+        assert np.array_equal(got[b][:, hit], want[:, hit], equal_nan=True)
+    cache.close()
