@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
     __shared__ unsigned strides[32 * kLaneSeqs];
     __shared__ unsigned valid_ring[kWarps][STAGES];
     __shared__ int qexp[HEADS];
-    __shared__ bool qfinite[HEADS];
+    __shared__ bool settles[HEADS];  // a score of the head that is NaN may not be (below)
     __shared__ bool last_block;
 
     const AttnArgs &A = P.a;
@@ -810,12 +810,13 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
 #pragma unroll
         for (int hh = 0; hh < HT; ++hh) {
             const int h = (tid >> 4) + hh * 8, lt = tid & 15;
-            float mx = 0.f, sum = 0.f;  // sum: 0, or NaN where q is not finite
+            float mx = 0.f, sum = 0.f;  // sum: 0, or NaN
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
                 qv[hh][i] = h < nh ? qv[hh][i] : 0.f;
                 mx = fmaxf(mx, fabsf(qv[hh][i]));
-                sum += qv[hh][i] * 0.f;
+                // A NaN in q is its answer, and so is an infinity but under a cap.
+                sum += A.softcap > 0.f && fabsf(qv[hh][i]) > FLT_MAX ? 0.f : qv[hh][i] * 0.f;
             }
             int e = 0;
 #pragma unroll
@@ -830,7 +831,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
             if (tid < 16 * NH) {  // (whole warps)
                 if (lt == 0) {
                     qexp[h] = e;
-                    qfinite[h] = sum == 0.f;
+                    settles[h] = sum == 0.f;
                 }
                 uint16_t *frag = reinterpret_cast<uint16_t *>(smem + hh * S::QF1);
                 uint16_t *frag3 =
@@ -1002,16 +1003,17 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
                 }
             const unsigned valid = valid_ring[warp][st];
             const int key0 = (sp.t0 + ta + warp + i * kWarps) * TILE;
-            // An infinite key component times pieces of q gives NaN where the
-            // product with q itself is infinite: settle it with q itself.
-            if (__any_sync(0xffffffffu, check != 0.f && qfinite[hd])) {
+            // An infinite component of a key times pieces of q, or an infinite one
+            // of q in pieces, gives NaN where the product with q itself is infinite:
+            // settle it with q itself.
+            if (__any_sync(0xffffffffu, check != 0.f && settles[hd])) {
                 const int64_t q0 = int64_t(seq) * A.ldq + int64_t(head0 + hd) * D;
 #pragma unroll
                 for (int u = 0; u < KT; ++u)
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         uint32_t row;
-                        if (!qfinite[hd] || hd >= nh || s[u][x] == s[u][x] ||
+                        if (!settles[hd] || hd >= nh || s[u][x] == s[u][x] ||
                             !row_of(key0 + u * kGroup + key_in(x), row))
                             continue;
                         float dot = 0.f;

@@ -54,3 +54,43 @@ def test_infinite_value_scale_beside_large_ones(D, group, before, beside, where)
         # infinite, or NaN for code 0
         assert np.array_equal(got[b][:, hit], want[:, hit], equal_nan=True)
     cache.close()
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16", "q8_0"])
+@pytest.mark.parametrize("group", [3, 8])
+@pytest.mark.parametrize("D", [64, 128])
+def test_infinite_query_under_a_cap(kind, group, D):
+    """cap * tanh of an infinite score is the cap: an infinite component of q
+    gives finite outputs, a NaN stays NaN, and neither touches other heads."""
+    rng = np.random.default_rng(group)
+    n, cap = 150, 5.0
+    table, n_pages, slots = ref.table_for([n], 16, rng)
+    pages = ref.Pages(q, kind, n_pages, 16, 1, D, rng)
+    if kind == "q8_0":  # (0 times infinity is NaN)
+        codes, scales = pages.raw[0]
+        codes[codes == 0] = 1
+        pages.val[0] = codes.astype(np.float64) * np.repeat(
+            scales[..., :D // 32].astype(np.float64), 32, axis=-1)
+    cache = pages.to_device(slots[0])
+    x = rng.standard_normal((1, group, D)).astype(np.float32)
+    x[0, 0, 7], x[0, 1, 33], x[0, 2, 40] = np.inf, -np.inf, np.nan
+    scale = float(np.float32(1 / math.sqrt(D)))
+    got, lse = cache.attend(torch.from_numpy(x).cuda(), torch.from_numpy(table).cuda(),
+                            torch.tensor([n], dtype=torch.int32, device="cuda"), scale=scale,
+                            softcap=cap, return_lse=True)
+    got, lse = got[0].double().cpu().numpy(), lse[0].double().cpu().numpy()
+    assert np.isnan(got[2]).all() and np.isnan(lse[2])
+    rest = [h for h in range(group) if h != 2]
+    k, v = pages.rows(0, slots[0]), pages.rows(1, slots[0])
+    with np.errstate(invalid="ignore"):
+        want, want_lse, _ = ref.attention(x[0].astype(np.float64), k, v, scale, cap)
+    _, _, size = ref.attention(np.where(np.isfinite(x[0]), x[0], 0).astype(np.float64), k, v, scale,
+                               cap)
+    tol, tol_lse = ref.attention_bound(size, D)
+    assert (np.abs(got - want)[rest] <= tol[rest, None]).all()
+    assert (np.abs(lse - want_lse)[rest] <= tol_lse[rest]).all()
+    # without a cap there is no answer
+    got = cache.attend(torch.from_numpy(x).cuda(), torch.from_numpy(table).cuda(),
+                       torch.tensor([n], dtype=torch.int32, device="cuda"), scale=scale)
+    assert torch.isnan(got[0, :3]).all() and torch.isfinite(got[0, 3:]).all()
+    cache.close()
