@@ -697,6 +697,14 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
                   pg * C.page.d;
             return unsigned(id) < C.n_pages;
         };
+        auto slow_dot = [&](int h, uint32_t row) {  // q of head h times a key
+            const int64_t q0 = int64_t(seq) * A.ldq + int64_t(head0 + h) * D;
+            float dot = 0.f;
+#pragma unroll 1
+            for (int d = 0; d < D; ++d)
+                dot += load_any(A.q, q0 + d, A.dtype) * value_at<KIND, D>(C.k, C.ks, row, d);
+            return dot;
+        };
         auto issue = [&](int i, int id) {
             const int first = (sp.t0 + ta + warp + i * kWarps) * TILE;
             const int st = i % STAGES;
@@ -1007,7 +1015,6 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
             // of q in pieces, gives NaN where the product with q itself is infinite:
             // settle it with q itself.
             if (__any_sync(0xffffffffu, check != 0.f && settles[hd])) {
-                const int64_t q0 = int64_t(seq) * A.ldq + int64_t(head0 + hd) * D;
 #pragma unroll
                 for (int u = 0; u < KT; ++u)
 #pragma unroll
@@ -1016,12 +1023,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
                         if (!settles[hd] || hd >= nh || s[u][x] == s[u][x] ||
                             !row_of(key0 + u * kGroup + key_in(x), row))
                             continue;
-                        float dot = 0.f;
-#pragma unroll 1
-                        for (int d = 0; d < D; ++d)
-                            dot += load_any(A.q, q0 + d, A.dtype) *
-                                   value_at<KIND, D>(C.k, C.ks, row, d);
-                        s[u][x] = dot * exp2i(qexp[hd]);
+                        s[u][x] = slow_dot(hd, row) * exp2i(qexp[hd]);
                     }
             }
             // scores in base 2
@@ -1201,40 +1203,6 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
             __syncwarp();
         }
         cp_wait<0>();
-        // An infinite value times pieces of a probability (some of them 0 or
-        // negative) gives NaN where the sum is infinite: those columns, if
-        // any, are settled by looking at the values again.
-        bool odd = false;
-#pragma unroll
-        for (int hh = 0; hh < HT; ++hh)
-#pragma unroll
-            for (int ds = 0; ds < D / 16; ++ds)
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    odd |= !(fabsf(O[hh][ds][x]) <= FLT_MAX);
-        if (__any_sync(0xffffffffu, odd)) {
-            float inf[D / 16][2] = {};  // sum of the column's infinities and NaNs
-            for (int i = 0; i < nw * TILE; ++i) {
-                uint32_t row;
-                if (!row_of((sp.t0 + ta + warp + i / TILE * kWarps) * TILE + i % TILE, row))
-                    continue;
-#pragma unroll
-                for (int ds = 0; ds < D / 16; ++ds)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const float v = value_at<KIND, D>(C.v, C.vs, row, dim_of<KIND>(ds, g, x));
-                        inf[ds][x] += fabsf(v) <= FLT_MAX ? 0.f : v;
-                    }
-            }
-#pragma unroll
-            for (int hh = 0; hh < HT; ++hh)
-#pragma unroll
-                for (int ds = 0; ds < D / 16; ++ds)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        if (!(fabsf(O[hh][ds][x]) <= FLT_MAX) && inf[ds][x >> 1] != 0.f)
-                            O[hh][ds][x] = inf[ds][x >> 1];
-        }
 #pragma unroll
         for (int hh = 0; hh < HT; ++hh) {
             l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 1);
@@ -1243,6 +1211,37 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
         __syncthreads();  // every warp is done with its ring: it becomes the joining space
 
         // ---- the warps' results joined
+        // An infinite value times pieces of a probability (some of them 0 or
+        // negative) gives NaN where the sum is infinite, and a key whose score is
+        // -infinity has probability 0, which makes an infinite value NaN: such
+        // sums, if any, are settled by looking at the values again.
+        auto settle_sum = [&](int h, int d, float4 &sum) {
+            float inf[4] = {};  // sums of the infinities and NaNs
+#pragma unroll 1
+            for (int j = (sp.t0 + ta) * TILE; j < (sp.t0 + tb) * TILE; ++j) {
+                uint32_t row;
+                if (!row_of(j, row))
+                    continue;
+                float v[4];
+                bool any = false;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    v[x] = value_at<KIND, D>(C.v, C.vs, row, d + x);
+                    v[x] = fabsf(v[x]) <= FLT_MAX ? 0.f : v[x];
+                    any |= v[x] != 0.f;
+                }
+                if (!any)
+                    continue;
+                const bool never = A.softcap == 0.f && slow_dot(h, row) * A.scale == -INFINITY;
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    inf[x] += never && v[x] != 0.f ? NAN : v[x];
+            }
+            sum.x = inf[0] != 0.f ? inf[0] : sum.x;
+            sum.y = inf[1] != 0.f ? inf[1] : sum.y;
+            sum.z = inf[2] != 0.f ? inf[2] : sum.z;
+            sum.w = inf[3] != 0.f ? inf[3] : sum.w;
+        };
         auto finish = [&](int h, int d, float4 sum, float M, float tot) {
             const float inv = tot == 0.f ? 0.f : 1.f / tot;
             store4_any(A.out, int64_t(seq) * A.ldo + int64_t(head0 + h) * D + d,
@@ -1300,6 +1299,8 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
                                  join + (w * HEADS + h) * S::OSTRIDE + d));
                 tot += f * join_ml[(w * HEADS + h) * 2 + 1];
             }
+            if (!(fabsf(sum.x) + fabsf(sum.y) + fabsf(sum.z) + fabsf(sum.w) <= FLT_MAX))
+                settle_sum(h, d, sum);
             if (whole) {
                 finish(h, d, sum, M, tot);
             } else {
@@ -1356,7 +1357,8 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
                         mn = fmaxf(mn, pm[j]);
-                    const float f = M == -INFINITY ? 0.f : ex2(M - mn);
+                    // (never 0: an infinite sum stays infinite)
+                    const float f = M == -INFINITY ? 0.f : fmaxf(ex2(M - mn), FLT_MIN);
                     sum = make_float4(sum.x * f, sum.y * f, sum.z * f, sum.w * f);
                     tot *= f;
                     M = mn;
@@ -1364,7 +1366,8 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
                     for (int j = 0; j < 16; ++j) {
                         if (c + j >= count)
                             continue;
-                        const float fj = pm[j] == -INFINITY ? 0.f : ex2(pm[j] - mn);
+                        const float fj =
+                            pm[j] == -INFINITY ? 0.f : fmaxf(ex2(pm[j] - mn), FLT_MIN);
                         add4(sum, fj, o[j]);
                         tot += fj * pl[j];
                     }
@@ -1485,7 +1488,7 @@ cudaError_t launch_heads(AttnParams &p, int sm_count, cudaStream_t s)
 // keys and values are fetched once for them, where the second operand's
 // instructions and registers cost less than the second fetch out of L2 (16
 // sequences of 4096 keys, 16 heads a key: head_dim 64 in f16 28 us, bf16 35, with
-// eight heads 37 and 40; f16 128: 51, with eight 55; bf16 128: 57, with eight 55).
+// eight heads 37 and 40; f16 128: 54, with eight 55; bf16 128: 57, with eight 55).
 template <Kind KIND, int D>
 cudaError_t launch_dim(AttnParams &p, int sm_count, cudaStream_t s)
 {

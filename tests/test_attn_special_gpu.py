@@ -94,3 +94,60 @@ def test_infinite_query_under_a_cap(kind, group, D):
                        torch.tensor([n], dtype=torch.int32, device="cuda"), scale=scale)
     assert torch.isnan(got[0, :3]).all() and torch.isfinite(got[0, 3:]).all()
     cache.close()
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16", "q8_0"])
+@pytest.mark.parametrize("group", [1, 4, 8, 16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,low", [(200, 0), (5000, 2500)])
+def test_infinite_value_of_a_key_that_is_never_attended_to(kind, group, D, n, low):
+    """A score of -infinity has probability 0, and 0 times infinity is NaN; an
+    infinite value elsewhere stays infinite, also of a key (or of `low` keys)
+    whose probability is too small for 32 bits."""
+    rng = np.random.default_rng(group)
+    table, n_pages, slots = ref.table_for([n], 16, rng)
+    pages = ref.Pages(q, kind, n_pages, 16, 1, D, rng)
+    place = [(s // 16, 0, s % 16) for s in slots[0]]
+    dead, far, seen = place[low + 37], place[90], place[low + 151]
+    small = place[:low] + [far]
+    x = rng.standard_normal((1, group, D)).astype(np.float32)
+    x[..., :32] = np.abs(x[..., :32]) + 1
+    if kind == "q8_0":
+        codes, scales = pages.raw[0]
+        codes[dead][:32], scales[dead][0] = -1, np.inf
+        for at in small:
+            codes[at][:32], scales[at][0] = -127, 60.0
+        values, vscales = pages.raw[1]
+        for at, block in ((dead, 0), (far, 1)) + ((seen, 1),) * (not low):
+            values[at][32 * block:32 * block + 32] = 3
+            vscales[at][block] = np.inf
+        zero, hit = slice(0, 32), slice(32, 64)
+        with np.errstate(invalid="ignore"):
+            for w in (0, 1):
+                pages.val[w] = pages.raw[w][0].astype(np.float64) * np.repeat(
+                    pages.raw[w][1][..., :D // 32].astype(np.float64), 32, axis=-1)
+    else:
+        k, v = pages.raw[0][0], pages.raw[1][0]
+        k[dead] = 0
+        k[dead][0] = -math.inf
+        for at in small:
+            k[at][:32] = -2000.0
+        v[dead][5] = v[far][9] = math.inf
+        v[seen][9] = 1.0 if low else math.inf  # (with low keys theirs is the only one)
+        zero, hit = slice(5, 6), slice(9, 10)
+        for w in (0, 1):
+            pages.val[w] = pages.raw[w][0].double().numpy()
+    cache = pages.to_device(slots[0])
+    scale = float(np.float32(1 / math.sqrt(D)))
+    got = cache.attend(torch.from_numpy(x).cuda(), torch.from_numpy(table).cuda(),
+                       torch.tensor([n], dtype=torch.int32, device="cuda"), scale=scale)
+    got = got[0].double().cpu().numpy()
+    assert np.isnan(got[:, zero]).all() and (got[:, hit] == math.inf).all()
+    keep = np.ones(D, bool)
+    keep[zero] = keep[hit] = False
+    sub = np.arange(n) != low + 37
+    k, v = pages.rows(0, slots[0])[sub], np.where(keep, pages.rows(1, slots[0])[sub], 0)
+    want, _, size = ref.attention(x[0].astype(np.float64), k, v, scale)
+    tol, _ = ref.attention_bound(size, D)
+    assert (np.abs(got - want)[:, keep] <= tol[:, None]).all()
+    cache.close()
