@@ -301,14 +301,9 @@ cudaError_t launch(LogitsArgs a, int sm_count, cudaStream_t s)
 {
     constexpr int N = 16 / sizeof(IO);
     const auto kern = adjust_kernel<IO, VEC>;
-    // Every block of a row scans its lists: as few parts as hold kLongest logits
-    // at most, then what fills the last wave of resident blocks (30 rows of 128256
-    // in bf16 with 2000 tokens: 9.9 us, with halved parts until each SM had four
-    // blocks 12.3; 8 rows in fp32 with 500: 7.0 and 8.1).
-    const int64_t fewest = (a.V + kLongest - 1) / kLongest, slots = int64_t(kResident) * sm_count;
-    const int64_t waves = (a.B * fewest + slots - 1) / slots;
-    a.parts = int(std::max(fewest, std::min(waves * slots / a.B, (a.V + 1023) / 1024)));
-    a.part = int((a.V + N + a.parts - 1) / a.parts + N - 1) / N * N;
+    const LogitsPlan plan = plan_logits(a.B, a.V, int(sizeof(IO)), sm_count);
+    a.parts = plan.parts;
+    a.part = plan.part;
     a.words = int(std::min<int64_t>(kWords, (int64_t(a.part) + N + 31) / 32 + 1));
     const bool named = a.n_history > 0 || a.n_biases > 0;
     const size_t smem = named ? (size_t(a.words) * 2 + kPlaces * 3) * 4 : 0;
@@ -335,6 +330,22 @@ cudaError_t launch_io(const LogitsArgs &a, int sm_count, cudaStream_t s)
 }
 
 } // namespace
+
+// Every block of a row scans its lists: as few parts as hold kLongest logits
+// at most, then what fills the last wave of resident blocks (30 rows of 128256
+// in bf16 with 2000 tokens: 9.9 us, with halved parts until each SM had four
+// blocks 12.3; 8 rows in fp32 with 500: 7.0 and 8.1).
+LogitsPlan plan_logits(int64_t B, int64_t V, int bytes, int sm_count)
+{
+    const int n = 16 / bytes;
+    const int64_t fewest = (V + kLongest - 1) / kLongest, slots = int64_t(kResident) * sm_count;
+    const int64_t waves = (B * fewest + slots - 1) / slots;
+    LogitsPlan p;
+    p.parts = int(std::max(fewest, std::min(waves * slots / B, (V + 1023) / 1024)));
+    p.part = int((V + n + p.parts - 1) / p.parts + n - 1) / n * n;
+    p.at_once = kPlaces;
+    return p;
+}
 
 cudaError_t launch_logits_adjust(const LogitsArgs &a, int sm_count, cudaStream_t s)
 {

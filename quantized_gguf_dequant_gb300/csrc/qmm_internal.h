@@ -502,6 +502,11 @@ struct LogitsArgs {
     // set by the launcher: blocks of a row, logits of a block, bitmap words
     int parts, part, words;
 };
+struct LogitsPlan {
+    int parts, part;  // blocks of a row, logits of a block
+    int at_once;      // named tokens that a block counts at a time
+};
+LogitsPlan plan_logits(int64_t B, int64_t V, int bytes, int sm_count);
 cudaError_t launch_logits_adjust(const LogitsArgs &a, int sm_count, cudaStream_t s);
 
 // Recording a refusal sentence for qmm_last_error() from other files.
