@@ -1465,21 +1465,24 @@ cudaError_t launch_warps(AttnParams &p, int sm_count, cudaStream_t s)
 // blocks, which overlap one another's starts and joins; with few items, whose
 // parts all have to be joined, one block of twelve (one sequence of 131071 keys:
 // 50.3 us, with four 53.5; 337 keys: 6.9 us, with four 8.0; Q8_0, four sequences of
-// 8000 keys: 14.4 us, with four 20.6).
+// 8000 keys: 14.4 us, with four 20.6).  Rows of 96, and 16-bit rows of 256: six
+// fill the shared memory better.
+constexpr int attn_warps(Kind k, int D)
+{
+    return D == 64 && k != kQ8 ? 8 : D == 96 || (D == 256 && k != kQ8) ? 6 : 4;
+}
+constexpr bool attn_has_twelve(int D, int heads) { return D == 128 && heads <= 8; }
+
 template <Kind KIND, int D, int HEADS>
 cudaError_t launch_heads(AttnParams &p, int sm_count, cudaStream_t s)
 {
-    if constexpr (KIND != kQ8 && D == 64)
-        return launch_warps<KIND, D, HEADS, 8>(p, sm_count, s);
-    if constexpr (D == 128 && HEADS <= 8) {
+    if constexpr (attn_has_twelve(D, HEADS)) {
         const int64_t items =
             int64_t(p.a.n_seqs) * p.a.c.n_heads * ((p.group + HEADS - 1) / HEADS);
         if (items * 4 <= sm_count)
             return launch_warps<KIND, D, HEADS, 12>(p, sm_count, s);
     }
-    // Rows of 96, and 16-bit rows of 256: six fill the shared memory better.
-    constexpr int W = D == 96 || (D == 256 && KIND != kQ8) ? 6 : 4;
-    return launch_warps<KIND, D, HEADS, W>(p, sm_count, s);
+    return launch_warps<KIND, D, HEADS, attn_warps(KIND, D)>(p, sm_count, s);
 }
 
 // Heads that a block takes together.  Up to four that share a key: their pieces
@@ -1489,12 +1492,17 @@ cudaError_t launch_heads(AttnParams &p, int sm_count, cudaStream_t s)
 // instructions and registers cost less than the second fetch out of L2 (16
 // sequences of 4096 keys, 16 heads a key: head_dim 64 in f16 28 us, bf16 35, with
 // eight heads 37 and 40; f16 128: 54, with eight 55; bf16 128: 57, with eight 55).
+constexpr bool attn_has_sixteen(Kind k, int D)
+{
+    return (D == 64 && k != kQ8) || (D == 128 && k == kF16);
+}
+
 template <Kind KIND, int D>
 cudaError_t launch_dim(AttnParams &p, int sm_count, cudaStream_t s)
 {
     if (p.group <= 4)
         return launch_heads<KIND, D, 4>(p, sm_count, s);
-    if constexpr ((KIND != kQ8 && D == 64) || (KIND == kF16 && D == 128)) {
+    if constexpr (attn_has_sixteen(KIND, D)) {
         if (p.group > 8)
             return launch_heads<KIND, D, 16>(p, sm_count, s);
     }

@@ -577,7 +577,10 @@ cudaError_t append_for_dim(const AppendArgs &a, int sm_count, cudaStream_t s)
                       grid, kThreads, s, a);
     switch (a.c.D) {
     case 64: return launch(append_kernel<KIND, IO, 64>, grid, kThreads, s, a);
-    case 96: return launch(append_kernel<KIND, IO, 96>, grid, kThreads, s, a);
+    case 96:
+        if constexpr (KIND != kQ8)  // (there append_regular says no)
+            return launch(append_kernel<KIND, IO, 96>, grid, kThreads, s, a);
+        break;
     case 128: return launch(append_kernel<KIND, IO, 128>, grid, kThreads, s, a);
     case 192: return launch(append_kernel<KIND, IO, 192>, grid, kThreads, s, a);
     case 256: return launch(append_kernel<KIND, IO, 256>, grid, kThreads, s, a);
