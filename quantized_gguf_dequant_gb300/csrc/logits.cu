@@ -40,7 +40,6 @@ constexpr int kThreads = 256;
 constexpr int kResident = 5;       // blocks of an SM
 constexpr int kLongest = 16384;    // logits of a part, at most
 constexpr int kAhead = 8;          // history tokens that a thread keeps in registers
-constexpr int kWords = 2048;       // bitmap words of a window, at most
 constexpr int kPlaces = 1024;      // named tokens counted at once
 constexpr uint32_t kNoOwner = 0xffffffffu;
 
@@ -234,110 +233,107 @@ __global__ void __launch_bounds__(kThreads, kResident) adjust_kernel(const __gri
         for (int64_t i = b0 + tid + kThreads; i < b1; i += kThreads)
             f(__ldg(P.bias_ids + i), uint32_t(i - b0));
     };
-    for (int w0 = lo; w0 < hi; w0 += 32 * P.words) {
-        const int span = min(hi - w0, 32 * P.words), words = (span + 31) / 32;
-        // A short part counts at the tokens' own places instead of their ranks.
-        const bool direct = span <= kPlaces;
-        uint32_t total = uint32_t(span);
-        if (tid == 0)
-            twice = 0;
-        if (!direct) {
-            for (int i = tid; i < words; i += kThreads)
-                bitmap[i] = 0u;
-            __syncthreads();
-            auto note = [&](int token) {
-                const unsigned at = unsigned(token) - unsigned(w0);
-                if (token >= 0 && at < unsigned(span))
-                    atomicOr(bitmap + (at >> 5), 1u << (at & 31));
-            };
-            each_said(note);
-            each_bias([&](int token, uint32_t) { note(token); });
-            __syncthreads();
-            // ranks: a thread takes `run` consecutive words
-            const int run = (words + kThreads - 1) / kThreads;
-            uint32_t mine = 0;
-            for (int k = 0; k < run; ++k) {
-                const int i = tid * run + k;
-                if (i < words) {
-                    before[i] = mine;
-                    mine += __popc(bitmap[i]);
-                }
+    const int span = hi - lo, words = (span + 31) / 32;  // (the bitmap holds a part)
+    // A short part counts at the tokens' own places instead of their ranks.
+    const bool direct = span <= kPlaces;
+    uint32_t total = uint32_t(span);
+    if (tid == 0)
+        twice = 0;
+    if (!direct) {
+        for (int i = tid; i < words; i += kThreads)
+            bitmap[i] = 0u;
+        __syncthreads();
+        auto note = [&](int token) {
+            const unsigned at = unsigned(token) - unsigned(lo);
+            if (token >= 0 && at < unsigned(span))
+                atomicOr(bitmap + (at >> 5), 1u << (at & 31));
+        };
+        each_said(note);
+        each_bias([&](int token, uint32_t) { note(token); });
+        __syncthreads();
+        // ranks: a thread takes `run` consecutive words
+        const int run = (words + kThreads - 1) / kThreads;
+        uint32_t mine = 0;
+        for (int k = 0; k < run; ++k) {
+            const int i = tid * run + k;
+            if (i < words) {
+                before[i] = mine;
+                mine += __popc(bitmap[i]);
             }
-            uint32_t upto = mine;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
-                upto += lane >= o ? v : 0u;
-            }
-            if (lane == 31)
-                warp_sum_[tid >> 5] = upto;
-            __syncthreads();
-            total = 0;
-#pragma unroll
-            for (int w = 0; w < kThreads / 32; ++w) {
-                upto += w < (tid >> 5) ? warp_sum_[w] : 0u;
-                total += warp_sum_[w];
-            }
-            for (int k = 0; k < run; ++k)
-                if (tid * run + k < words)
-                    before[tid * run + k] += upto - mine;
         }
-        // named tokens by rank, kPlaces at a time
-        for (uint32_t first = 0; first < total; first += kPlaces) {
-            const uint32_t n = min(uint32_t(kPlaces), total - first);
-            for (uint32_t i = tid; i < n; i += kThreads) {
-                counts[i] = 0u;
-                owner[i] = kNoOwner;
+        uint32_t upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
+            upto += lane >= o ? v : 0u;
+        }
+        if (lane == 31)
+            warp_sum_[tid >> 5] = upto;
+        __syncthreads();
+        total = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            upto += w < (tid >> 5) ? warp_sum_[w] : 0u;
+            total += warp_sum_[w];
+        }
+        for (int k = 0; k < run; ++k)
+            if (tid * run + k < words)
+                before[tid * run + k] += upto - mine;
+    }
+    // named tokens by rank, kPlaces at a time
+    for (uint32_t first = 0; first < total; first += kPlaces) {
+        const uint32_t n = min(uint32_t(kPlaces), total - first);
+        for (uint32_t i = tid; i < n; i += kThreads) {
+            counts[i] = 0u;
+            owner[i] = kNoOwner;
+        }
+        __syncthreads();
+        auto place = [&](int token) {  // its place, or kPlaces and more
+            const unsigned at = unsigned(token) - unsigned(lo);
+            if (token < 0 || at >= unsigned(span))
+                return uint32_t(kPlaces);
+            if (direct)
+                return at;
+            return before[at >> 5] + __popc(bitmap[at >> 5] & ((1u << (at & 31)) - 1u)) - first;
+        };
+        each_said([&](int token) {
+            const uint32_t p = place(token);
+            if (p < kPlaces) {
+                atomicAdd(counts + p, 1u);
+                ids[p] = token;
             }
-            __syncthreads();
-            auto place = [&](int token) {  // its place, or kPlaces and more
-                const unsigned at = unsigned(token) - unsigned(w0);
-                if (token < 0 || at >= unsigned(span))
-                    return uint32_t(kPlaces);
-                if (direct)
-                    return at;
-                return before[at >> 5] + __popc(bitmap[at >> 5] & ((1u << (at & 31)) - 1u)) - first;
-            };
-            each_said([&](int token) {
-                const uint32_t p = place(token);
-                if (p < kPlaces) {
-                    atomicAdd(counts + p, 1u);
-                    ids[p] = token;
-                }
-            });
-            each_bias([&](int token, uint32_t i) {
-                const uint32_t p = place(token);
-                if (p < kPlaces) {
-                    ids[p] = token;
-                    if (atomicMin(owner + p, i) != kNoOwner)
-                        twice = 1;
-                }
-            });
-            __syncthreads();
-            const bool again = twice;
-            if (again) {  // in list order by the first warp
-                if (tid < 32)
-                    add_in_order(P, b0, b1, owner, sums, place);
-                __syncthreads();
+        });
+        each_bias([&](int token, uint32_t i) {
+            const uint32_t p = place(token);
+            if (p < kPlaces) {
+                ids[p] = token;
+                if (atomicMin(owner + p, i) != kNoOwner)
+                    twice = 1;
             }
-            for (uint32_t p = tid; p < n; p += kThreads) {
-                const uint32_t c = counts[p], first_bias = owner[p];
-                if (direct && c == 0 && first_bias == kNoOwner)
-                    continue;
-                const int token = direct ? w0 + int(p) : int(ids[p]);
-                float z = load1(in + token);
-                const bool banned = mask && !(mask_bits(mask, token, V) & 1u);
-                if (c) {
-                    z = z > 0.f ? __fdiv_rn(z, r) : __fmul_rn(z, r);
-                    z = __fsub_rn(z, __fadd_rn(presence, __fmul_rn(frequency, float(c))));
-                }
-                if (first_bias != kNoOwner) {
-                    z = __fadd_rn(z, again ? sums[p] : __ldg(P.bias_values + b0 + first_bias));
-                }
-                store1(out + token, banned ? -INFINITY : z);
-            }
+        });
+        __syncthreads();
+        const bool again = twice;
+        if (again) {  // in list order by the first warp
+            if (tid < 32)
+                add_in_order(P, b0, b1, owner, sums, place);
             __syncthreads();
         }
+        for (uint32_t p = tid; p < n; p += kThreads) {
+            const uint32_t c = counts[p], first_bias = owner[p];
+            if (direct && c == 0 && first_bias == kNoOwner)
+                continue;
+            const int token = direct ? lo + int(p) : int(ids[p]);
+            float z = load1(in + token);
+            const bool banned = mask && !(mask_bits(mask, token, V) & 1u);
+            if (c) {
+                z = z > 0.f ? __fdiv_rn(z, r) : __fmul_rn(z, r);
+                z = __fsub_rn(z, __fadd_rn(presence, __fmul_rn(frequency, float(c))));
+            }
+            if (first_bias != kNoOwner)
+                z = __fadd_rn(z, again ? sums[p] : __ldg(P.bias_values + b0 + first_bias));
+            store1(out + token, banned ? -INFINITY : z);
+        }
+        __syncthreads();
     }
 }
 
@@ -349,7 +345,7 @@ cudaError_t launch(LogitsArgs a, int sm_count, cudaStream_t s)
     const LogitsPlan plan = plan_logits(a.B, a.V, int(sizeof(IO)), sm_count);
     a.parts = plan.parts;
     a.part = plan.part;
-    a.words = int(std::min<int64_t>(kWords, (int64_t(a.part) + N + 31) / 32 + 1));
+    a.words = (a.part + N + 31) / 32 + 1;
     const bool named = a.n_history > 0 || a.n_biases > 0;
     const size_t smem =
         named ? (size_t(a.words) * 2 + kPlaces * (a.n_biases > 0 ? 4 : 3)) * 4 : 0;
