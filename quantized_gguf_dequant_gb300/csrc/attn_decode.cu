@@ -10,7 +10,12 @@ bool attn_takes_head_dim(int D)
     return D == 64 || D == 96 || D == 128 || D == 192 || D == 256;
 }
 
-size_t attn_partial_floats(int D) { return size_t(kAttnHeads) * size_t(D + 2); }
+AttnSpace attn_space(int type, int D)
+{
+    return type == QMM_F16 ? attn_space_f16(D)
+           : type == QMM_BF16 ? attn_space_bf16(D)
+                              : attn_space_q8(D);
+}
 
 cudaError_t launch_attn_decode(const AttnArgs &a, int sm_count, cudaStream_t s)
 {

@@ -8,4 +8,6 @@ cudaError_t launch_attn_f16(AttnParams &p, int sm_count, cudaStream_t s)
     return launch_kind<kF16>(p, sm_count, s);
 }
 
+AttnSpace attn_space_f16(int D) { return space_kind<kF16>(D); }
+
 } // namespace qmm

@@ -1445,7 +1445,8 @@ cudaError_t launch_warps(AttnParams &p, int sm_count, cudaStream_t s)
     const int64_t longest = std::min<int64_t>(p.a.ld_table * p.a.c.page_size, kMostKeys);
     const int64_t items = int64_t(p.a.n_seqs) * p.items;
     const int64_t units = items * ((longest + Sh::TILE - 1) / Sh::TILE + 1 + Sh::COST);
-    int64_t grid = std::min<int64_t>(int64_t(occ) * sm_count, p.a.max_blocks);
+    // (the workspace is sized to Shape's blocks: attn_space)
+    int64_t grid = int64_t(std::min<int>(occ, Sh::BLOCKS)) * sm_count;
     grid = std::max<int64_t>(1, std::min(grid, std::max(items, units / Sh::MIN_UNITS) + 1));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(grid));
@@ -1507,6 +1508,38 @@ cudaError_t launch_dim(AttnParams &p, int sm_count, cudaStream_t s)
             return launch_heads<KIND, D, 16>(p, sm_count, s);
     }
     return launch_heads<KIND, D, 8>(p, sm_count, s);
+}
+
+// What an SM's blocks need of the workspace, whichever form is launched: two
+// partial results a block.
+template <Kind KIND, int D, int HEADS, int WARPS>
+constexpr AttnSpace with_form(AttnSpace s)
+{
+    using Sh = Shape<KIND, D, HEADS, WARPS>;
+    return {std::max(s.blocks, int(Sh::BLOCKS)),
+            std::max(s.floats, size_t(2) * Sh::BLOCKS * HEADS * (D + 2))};
+}
+template <Kind KIND, int D>
+constexpr AttnSpace space_dim()
+{
+    constexpr int W = attn_warps(KIND, D);
+    AttnSpace s = with_form<KIND, D, 8, W>(with_form<KIND, D, 4, W>({0, 0}));
+    if constexpr (attn_has_twelve(D, 8))
+        s = with_form<KIND, D, 8, 12>(with_form<KIND, D, 4, 12>(s));
+    if constexpr (attn_has_sixteen(KIND, D))
+        s = with_form<KIND, D, 16, W>(s);
+    return s;
+}
+template <Kind KIND>
+AttnSpace space_kind(int D)
+{
+    switch (D) {
+    case 64: return space_dim<KIND, 64>();
+    case 96: return space_dim<KIND, 96>();
+    case 128: return space_dim<KIND, 128>();
+    case 192: return space_dim<KIND, 192>();
+    default: return space_dim<KIND, 256>();
+    }
 }
 
 template <Kind KIND>

@@ -8,4 +8,6 @@ cudaError_t launch_attn_q8(AttnParams &p, int sm_count, cudaStream_t s)
     return launch_kind<kQ8>(p, sm_count, s);
 }
 
+AttnSpace attn_space_q8(int D) { return space_kind<kQ8>(D); }
+
 } // namespace qmm

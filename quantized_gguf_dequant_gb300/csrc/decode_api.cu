@@ -15,8 +15,6 @@ using qmm::record_error;
 
 namespace {
 
-constexpr int kBlocksPerSm = 4;  // attention blocks that the workspace has room for
-
 qmm_status cuda_error(cudaError_t e, const char *fn)
 {
     return record_error(QMM_ERR_CUDA, "%s: CUDA error %d (%s): %s", fn, int(e),
@@ -193,9 +191,10 @@ qmm_status qmm_kv_create(int32_t type, int64_t n_pages, int32_t page_size, int32
             delete c;
             return cuda_error(e, fn);
         }
-        c->max_blocks = c->sm_count * kBlocksPerSm;
+        const qmm::AttnSpace space = qmm::attn_space(type, head_dim);
+        c->max_blocks = c->sm_count * space.blocks;
         const size_t words = size_t(c->max_blocks) * 3 + 64;  // tickets, status word
-        c->ws_bytes = size_t(2) * c->max_blocks * qmm::attn_partial_floats(head_dim) * 4;
+        c->ws_bytes = size_t(c->sm_count) * space.floats * 4;
         void *p = nullptr;
         e = cudaMalloc(&p, c->ws_bytes + words * 4);
         if (e != cudaSuccess) {

@@ -449,7 +449,6 @@ struct KvReadArgs {
 cudaError_t launch_kv_read(const KvReadArgs &a, int sm_count, cudaStream_t s);
 
 // Attention of one new token per sequence (attn_decode.cu).
-constexpr int kAttnHeads = 16;  // query heads of one kv head that a block takes at most
 struct AttnArgs {
     KvView c;
     int type, dtype;
@@ -475,9 +474,17 @@ struct AttnParams {
     int items;          // kv heads * head tiles
 };
 bool attn_takes_head_dim(int D);
-size_t attn_partial_floats(int D);  // floats of one partial result
+// The most resident blocks of an SM, and the floats of their partial results.
+struct AttnSpace {
+    int blocks;
+    size_t floats;
+};
+AttnSpace attn_space(int type, int D);
 cudaError_t launch_attn_decode(const AttnArgs &a, int sm_count, cudaStream_t s);
 // attn_f16.cu, attn_bf16.cu, attn_q8.cu
+AttnSpace attn_space_f16(int D);
+AttnSpace attn_space_bf16(int D);
+AttnSpace attn_space_q8(int D);
 cudaError_t launch_attn_f16(AttnParams &p, int sm_count, cudaStream_t s);
 cudaError_t launch_attn_bf16(AttnParams &p, int sm_count, cudaStream_t s);
 cudaError_t launch_attn_q8(AttnParams &p, int sm_count, cudaStream_t s);
