@@ -1299,7 +1299,9 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
                                  join + (w * HEADS + h) * S::OSTRIDE + d));
                 tot += f * join_ml[(w * HEADS + h) * 2 + 1];
             }
-            if (!(fabsf(sum.x) + fabsf(sum.y) + fabsf(sum.z) + fabsf(sum.w) <= FLT_MAX))
+            // (where the probabilities are NaN there is nothing to settle)
+            if (!(fabsf(sum.x) + fabsf(sum.y) + fabsf(sum.z) + fabsf(sum.w) <= FLT_MAX) &&
+                tot == tot)
                 settle_sum(h, d, sum);
             if (whole) {
                 finish(h, d, sum, M, tot);
