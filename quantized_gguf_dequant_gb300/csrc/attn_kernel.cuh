@@ -895,7 +895,8 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
             qscale[hh] = A.scale * exp2i(-qexp[hd]);
             slope[hh] = A.alibi && hd < nh ? __ldg(A.alibi + head0 + hd) * kLog2e : 0.f;
         }
-        const float cap_inv = A.softcap > 0.f ? 1.f / A.softcap : 0.f;
+        // (a cap below 2^-128 has no finite reciprocal, and a score of 0 stays 0)
+        const float cap_inv = A.softcap > 0.f ? fminf(1.f / A.softcap, FLT_MAX) : 0.f;
         // f16 probabilities are carried 2^14 times as large, clear of its subnormals
         constexpr float kBias = KIND == kF16 ? 14.f : 0.f;
         float m[HT], l[HT];  // of head hd

@@ -151,3 +151,25 @@ def test_infinite_value_of_a_key_that_is_never_attended_to(kind, group, D, n, lo
     tol, _ = ref.attention_bound(size, D)
     assert (np.abs(got - want)[:, keep] <= tol[:, None]).all()
     cache.close()
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16", "q8_0"])
+@pytest.mark.parametrize("cap", [1e-30, 1e-39, 1e-45])
+def test_caps_of_any_size(kind, cap):
+    """A score of 0 stays 0 under a cap whose reciprocal is beyond 32 bits."""
+    rng = np.random.default_rng(5)
+    n, D = 100, 64
+    table, n_pages, slots = ref.table_for([n], 16, rng)
+    pages = ref.Pages(q, kind, n_pages, 16, 1, D, rng)
+    zero = (slots[0][11] // 16, 0, slots[0][11] % 16)
+    pages.raw[0][0][zero] = 0
+    pages.val[0][zero] = 0
+    cache = pages.to_device(slots[0])
+    x = rng.standard_normal((1, 4, D)).astype(np.float32)
+    got = cache.attend(torch.from_numpy(x).cuda(), torch.from_numpy(table).cuda(),
+                       torch.tensor([n], dtype=torch.int32, device="cuda"), scale=0.125, softcap=cap)
+    want, _, size = ref.attention(x[0].astype(np.float64), pages.rows(0, slots[0]),
+                                  pages.rows(1, slots[0]), 0.125, float(np.float32(cap)))
+    tol, _ = ref.attention_bound(size, D)
+    assert (np.abs(got[0].double().cpu().numpy() - want) <= tol[:, None]).all()
+    cache.close()
