@@ -428,8 +428,12 @@ typedef struct {
  * leaves its keys out, a length that is negative or beyond ld_table pages (or
  * 2^31 - 2^16 keys) is cut to fit; either sets QMM_ERR_PAGE in the status word.  Slots out of
  * range are never read, whatever they hold.
- * Computed in fp32 precision throughout (the cache's values are exact
- * operands); bitwise repeatable for the same lengths. */
+ * Sums, maxima and exponentials are fp32. The cache's values are exact
+ * operands; q and the probabilities enter in 16-bit pieces that hold 22 bits of
+ * each (QMM_BF16: 24).  Against 64 bits, root mean squares: a score is off by
+ * less than 2^-24 of sum |q k|, an output by less than 5 * 2^-24 of sum p |v|.
+ * Infinities in q, keys and values give what the formula gives, scores that are
+ * all -infinity what no keys give.  Bitwise repeatable for the same lengths. */
 QMM_API qmm_status qmm_attn_decode(qmm_kv_t kv, int32_t dtype, int64_t n_seqs, int32_t n_q_heads,
                                    const void *q, int64_t ldq, const int32_t *page_table,
                                    int64_t ld_table, const int32_t *lens, const qmm_attn *attn,

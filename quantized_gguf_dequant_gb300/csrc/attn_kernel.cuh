@@ -21,7 +21,7 @@
 // Measured on one GB300 (bytes of keys, values, q and out; the card copies
 // 6.77 TB/s): 16 sequences of 2000-4001 keys, 32 heads on 8 of 128, bf16: 32.7 us,
 // 5.0 TB/s; 64 sequences of 8192-16384 keys in Q8_0: 287 us, 5.7 TB/s (bound by
-// issuing instructions: about 490 a 16 keys); one of 131071 keys, 32 heads on 4, f16,
+// issuing instructions: about 500 a 16 keys); one of 131071 keys, 32 heads on 4, f16,
 // capped: 50 us, 5.3 TB/s; 24 with windows of 1024, 12 heads of 64: 16.3 us,
 // 4.3 TB/s; one of 337 keys: 6.8 us.  Of the 32.7 us the loads take about 22, at the
 // card's rate; 2.3 go by until the first tile is asked for (lengths, page ids,
@@ -38,10 +38,14 @@
 //
 // Products run on mma.sync m16n8k16 (two operands of 16 bits, fp32 sums): at
 // one new token the tensor work is a fraction of the load time, and eight
-// heads fill its n (values) or half its m (keys).  Activations stay in fp32
-// precision: q is split into 16-bit pieces whose sum is q to 22 bits or more
-// (two pieces after a power-of-two normalisation for f16 operands, three for
-// bf16), and so are the probabilities.  The first two q pieces share one
+// heads fill its n (values) or half its m (keys).  q is split into 16-bit pieces,
+// and so are the probabilities: two after a power-of-two normalisation for f16
+// operands, which hold 22 bits of each number, three for bf16, which hold 24.  A
+// third f16 piece would be half as many products again, against errors that the
+// sums make anyway: root mean squares against 64 bits are 0.15 to 0.25 units of
+// 2^-24 sum |q k| for a score (f16 keys, whose products are longer, 0.5 to 0.9) and
+// 1 to 1.3 of 2^-24 sum p |v| for an output of four keys (f16 1.9 to 2.4);
+// exponentials are ex2.approx, 2 units.  The first two q pieces share one
 // instruction: piece 0 in rows 0-7, piece 1 in rows 8-15; with four heads an
 // instruction takes up to four pieces.
 //   QK:  S[16 = (piece, head)][8 keys] += Q[16][16 d] K[8 keys][16 d]^T
@@ -473,7 +477,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
     // up to four neighbouring sequences a lane, where the general plan's barriers
     // and loops cost more (128 sequences of 100 keys, 2 heads of 64: 11.4 -> 6.0 us;
     // 48 of 1000, one head of 128: 14.9 -> 12.8).  Not for Q8_0: its kernel lost
-    // registers of the main loop to this (64 sequences: 276 -> 294 us).
+    // registers of the main loop to this (64 sequences 294 us, without it 276 then).
     bool some = KIND != kQ8 && A.n_seqs > 32 && A.n_seqs <= 32 * kLaneSeqs;
     if (some) {
         const int each = (A.n_seqs + 31) / 32;  // sequences of a lane
@@ -505,7 +509,7 @@ __global__ void __launch_bounds__(Shape<KIND, D, HEADS, WARPS>::THREADS,
         }
         if (some) {
             per = share(total, most);
-            // With someer items than blocks, shares a little larger may let every
+            // With fewer items than blocks, shares a little larger may let every
             // block keep to one item: a second one costs it another start and join.
             if (per < (1 << 23)) {
                 const unsigned p0 = unsigned(per);

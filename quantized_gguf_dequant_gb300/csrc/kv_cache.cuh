@@ -20,7 +20,9 @@
 
 namespace qmm {
 
-// n / d for 0 <= n < 2^31 by one high product: q = (umulhi(mul, n) + n) >> shift.
+// n / d for 0 <= n < 2^31 by one high product, after Granlund and Montgomery,
+// "Division by Invariant Integers using Multiplication" (1994):
+// q = (umulhi(mul, n) + n) >> shift.
 __device__ __forceinline__ uint32_t fast_div(const FastDiv &f, uint32_t n)
 {
     return (__umulhi(f.mul, n) + n) >> f.shift;
